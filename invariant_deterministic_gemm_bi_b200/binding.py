@@ -1,5 +1,5 @@
-"""Thin ctypes binding of libbigemm (include/bi_gemm.h, bi_moe.h, bi_attention.h, bi_quantize.h),
-same names as the C ABI.
+"""Thin ctypes binding of libbigemm (include/bi_gemm.h, bi_moe.h, bi_attention.h, bi_quantize.h,
+bi_kv_cache.h, bi_paged_attention.h), same names as the C ABI.
 
 Argument marshalling only: every function takes torch tensors (device memory owned by torch)
 or raw integers, passes their pointers, strides and the current CUDA stream to the C entry
@@ -43,6 +43,8 @@ EXPORTED = [
     "bi_moe_route_topk", "bi_moe_dispatch", "bi_moe_gather_rows", "bi_moe_combine",
     "bi_decode_attention", "bi_decode_attention_workspace_bytes",
     "bi_quantize_e2m1",
+    "bi_kv_block_tables", "bi_kv_append_e4m3",
+    "bi_paged_decode_attention", "bi_paged_decode_attention_workspace_bytes",
 ]
 
 
@@ -75,6 +77,16 @@ class HostGemm(ctypes.Structure):
         ("B", ctypes.c_void_p), ("ldb", ctypes.c_int64), ("C_host", ctypes.c_void_p),
         ("ldc", ctypes.c_int64), ("scale_a_host", ctypes.c_void_p), ("ld_sa", ctypes.c_int64),
         ("scale_b", ctypes.c_void_p),
+    ]
+
+
+class KvCacheView(ctypes.Structure):
+    """bi_kv_cache_t: the pools of a paged 8-bit key/value cache."""
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int),
+        ("num_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("page_stride", ctypes.c_int64),
+        ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
     ]
 
 
@@ -152,6 +164,17 @@ def load_library(path: str = LIB_PATH):
                                         vp, ctypes.c_size_t, vp, vp]
     lib.bi_quantize_e2m1.restype = i32
     lib.bi_quantize_e2m1.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, i64, vp]
+    pc = ctypes.POINTER(KvCacheView)
+    lib.bi_kv_block_tables.restype = i32
+    lib.bi_kv_block_tables.argtypes = [vp, vp, i64, i32, vp, i64, vp, vp, i64, i64, vp, vp, vp, vp, i64,
+                                       vp, vp, vp]
+    lib.bi_kv_append_e4m3.restype = i32
+    lib.bi_kv_append_e4m3.argtypes = [pc, vp, i64, vp, i64, vp, i64, vp]
+    lib.bi_paged_decode_attention_workspace_bytes.restype = ctypes.c_size_t
+    lib.bi_paged_decode_attention_workspace_bytes.argtypes = [i64, i32, i32, i64]
+    lib.bi_paged_decode_attention.restype = i32
+    lib.bi_paged_decode_attention.argtypes = [pc, vp, i64, vp, i64, i64, vp, i64, i32, ctypes.c_float,
+                                              i64, vp, ctypes.c_size_t, vp, i64, vp, vp]
     if path == LIB_PATH:
         _LIB = lib
     return lib
@@ -472,3 +495,138 @@ def bi_quantize_e2m1(W, w_scale, Q, w_zero=None, stream=None):
                                          _stream_handle(stream))
     _check(st, "bi_quantize_e2m1")
     return Q
+
+
+# ---------------------------------------------------------------------------------------------
+# Paged 8-bit key/value cache (include/bi_kv_cache.h, include/bi_paged_attention.h)
+# ---------------------------------------------------------------------------------------------
+
+def _on_current_device(*tensors):
+    """The C calls launch on the current device: a tensor of another one is refused here."""
+    import torch
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"every tensor must be on the current device cuda:{dev}")
+
+
+def _int32_vectors(**tensors):
+    import torch
+    for name, t in tensors.items():
+        if t is not None and (t.dtype is not torch.int32 or not t.is_contiguous()):
+            raise TypeError(f"{name} must be a contiguous int32 tensor")
+
+
+def _block_table(table):
+    import torch
+    if table.dtype is not torch.int32 or table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise TypeError("block_table must be int32 [B, max_pages] with a unit inner stride")
+    # a one-row table's pitch is never used
+    return max(table.stride(0), table.shape[1])
+
+
+def _heads_rows(name, x, heads, dim):
+    """The row pitch of bf16 [rows, heads, dim] whose rows are contiguous (any pitch)."""
+    import torch
+    if x.dtype is not torch.bfloat16 or x.dim() != 3 or x.shape[1] != heads or x.shape[2] != dim:
+        raise TypeError(f"{name} must be bf16 [rows, {heads}, {dim}]")
+    if x.numel() and (x.stride(2) != 1 or (heads > 1 and x.stride(1) != dim)):
+        raise TypeError(f"{name}: the {heads} x {dim} values of a row must be contiguous")
+    return x.stride(0) if x.shape[0] > 1 else heads * dim
+
+
+class KvCache:
+    """Pools of a paged 8-bit cache (bi_kv_cache_t), kept alive by this handle.
+
+    k, v: e4m3 or uint8 [pages, page_size, heads, head_dim] with equal strides and contiguous
+    head_dim (for [page, head, token, dim] memory pass ``t.transpose(1, 2)``); k_scale, v_scale:
+    fp32 [pages, heads], contiguous.  Nothing is copied."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        import torch
+        for t in (k, v):
+            if t.dtype not in (torch.uint8, torch.float8_e4m3fn) or t.dim() != 4 or t.stride(3) != 1:
+                raise TypeError("k and v must be uint8 or e4m3 [pages, page_size, heads, head_dim] with a "
+                                "unit inner stride")
+        if k.shape != v.shape or k.stride() != v.stride():
+            raise ValueError("k and v must have equal shapes and strides")
+        for t in (k_scale, v_scale):
+            if t.dtype is not torch.float32 or t.shape != (k.shape[0], k.shape[2]) or not t.is_contiguous():
+                raise TypeError("k_scale and v_scale must be contiguous fp32 [pages, heads]")
+        if len({t.device for t in (k, v, k_scale, v_scale)}) != 1:
+            raise ValueError("the pools and their scales must be on one device")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.num_pages, self.page_size, self.num_heads, self.head_dim = k.shape
+        # the stride of an axis of one element is never used: give it the least that is valid
+        ts = k.stride(1)
+        hs = k.stride(2) if self.num_heads > 1 else self.head_dim
+        ps = k.stride(0) if self.num_pages > 1 else \
+            (self.page_size - 1) * ts + (self.num_heads - 1) * hs + self.head_dim
+        self.view = KvCacheView(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), self.num_pages,
+                                self.page_size, self.num_heads, self.head_dim, ps, ts, hs)
+        self.ref = ctypes.pointer(self.view)
+
+
+def bi_kv_block_tables(ctx_lens, new_lens, page_size: int, free_pages, free_count, block_table, seq_lens,
+                       token_offsets, slot_map, free_left, status, positions=None, stream=None):
+    """Block tables and slot maps of one step from the requests' lengths (all int32, device):
+    ctx_lens, new_lens (-1: ended), seq_lens [B]; free_pages [capacity], a stack of free_count [1]
+    pages; block_table [B, max_pages]; token_offsets [B+1]; slot_map, positions [max_tokens];
+    free_left, status [1].  seq_lens may be ctx_lens and free_left may be free_count."""
+    B = ctx_lens.numel()
+    _int32_vectors(ctx_lens=ctx_lens, new_lens=new_lens, free_pages=free_pages, free_count=free_count,
+                   seq_lens=seq_lens, token_offsets=token_offsets, slot_map=slot_map, free_left=free_left,
+                   status=status, positions=positions)
+    ld = _block_table(block_table)
+    if new_lens.numel() != B or seq_lens.numel() != B or token_offsets.numel() != B + 1 or \
+            block_table.shape[0] != B or free_count.numel() != 1 or free_left.numel() != 1 or \
+            status.numel() != 1 or (positions is not None and positions.numel() != slot_map.numel()):
+        raise ValueError("lengths of the arrays do not agree")
+    _on_current_device(ctx_lens, new_lens, free_pages, free_count, block_table, seq_lens, token_offsets,
+                       slot_map, free_left, status, positions)
+    _check(load_library().bi_kv_block_tables(
+        _ptr(ctx_lens), _ptr(new_lens), B, page_size, _ptr(free_pages), free_pages.numel(), _ptr(free_count),
+        _ptr(block_table), ld, block_table.shape[1], _ptr(seq_lens), _ptr(token_offsets), _ptr(slot_map),
+        _ptr(positions), slot_map.numel(), _ptr(free_left), _ptr(status), _stream_handle(stream)),
+        "bi_kv_block_tables")
+
+
+def bi_kv_append_e4m3(cache: KvCache, K, V, slot_map, stream=None):
+    """Write bf16 K, V [T, heads, head_dim] (rows of any pitch) to the slots slot_map int32 [T]."""
+    T = K.shape[0]
+    if V.shape[0] != T or slot_map.numel() != T:
+        raise ValueError("K, V and slot_map must have the same number of rows")
+    ldk = _heads_rows("K", K, cache.num_heads, cache.head_dim)
+    ldv = _heads_rows("V", V, cache.num_heads, cache.head_dim)
+    _int32_vectors(slot_map=slot_map)
+    _on_current_device(cache.k, K, V, slot_map)
+    _check(load_library().bi_kv_append_e4m3(cache.ref, _ptr(K), ldk, _ptr(V), ldv, _ptr(slot_map), T,
+                                            _stream_handle(stream)), "bi_kv_append_e4m3")
+
+
+def bi_paged_decode_attention_workspace_bytes(B: int, Hq: int, D: int, max_len: int) -> int:
+    return int(load_library().bi_paged_decode_attention_workspace_bytes(B, Hq, D, max_len))
+
+
+def bi_paged_decode_attention(cache: KvCache, Q, block_table, seq_lens, O, scale: float, workspace=None,
+                              lse=None, window: int = 0, stream=None):
+    """Q [B, Hq, D] bf16, block_table int32 [B, max_pages], seq_lens int32 [B] -> O [B, Hq, D] bf16
+    and, if given, lse fp32 [B, Hq].  workspace: a device tensor of at least
+    bi_paged_decode_attention_workspace_bytes(B, Hq, D, max_pages * page_size) bytes."""
+    import torch
+    B, Hq = Q.shape[0], Q.shape[1]
+    ldq = _heads_rows("Q", Q, Hq, cache.head_dim)
+    ldo = _heads_rows("O", O, Hq, cache.head_dim)
+    ld = _block_table(block_table)
+    _int32_vectors(seq_lens=seq_lens)
+    if O.shape[0] != B or block_table.shape[0] != B or seq_lens.numel() != B:
+        raise ValueError("Q, O, block_table and seq_lens must have the same number of rows")
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (B, Hq) or not lse.is_contiguous()):
+        raise TypeError("lse must be contiguous fp32 [B, Hq]")
+    _on_current_device(cache.k, Q, block_table, seq_lens, O, workspace, lse)
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load_library().bi_paged_decode_attention(
+        cache.ref, _ptr(Q), ldq, _ptr(block_table), ld, block_table.shape[1], _ptr(seq_lens), B, Hq, scale,
+        window, _ptr(workspace), nbytes, _ptr(O), ldo, _ptr(lse), _stream_handle(stream)),
+        "bi_paged_decode_attention")
+    return O

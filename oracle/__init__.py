@@ -1,5 +1,6 @@
 """CPU oracle for the batch-invariant GEMM -- test infrastructure only (see ``oracle.py``; the MoE
-steps around the grouped GEMM are in ``moe.py``, the decode attention in ``attention.py``)."""
+steps around the grouped GEMM are in ``moe.py``, the decode attention in ``attention.py``, the paged
+8-bit cache in ``kv_cache.py``)."""
 from .oracle import (  # noqa: F401
     bf16_to_f64,
     OracleLib,
@@ -22,4 +23,4 @@ from .oracle import (  # noqa: F401
     grouped_gemm_bf16_exact_integers,
     quantize_e2m1,
 )
-from . import attention, moe  # noqa: F401,E402
+from . import attention, kv_cache, moe  # noqa: F401,E402

@@ -53,7 +53,8 @@ size_t bi_paged_decode_attention_workspace_bytes(int64_t B, int Hq, int D, int64
  * page_size) bytes, 16-byte aligned (NULL when that is 0).  The call overwrites it; calls that may
  * run at the same time need workspaces of their own.
  * Q and O 16-byte aligned, ldq and ldo multiples of 8 and >= Hq * head_dim; other arrays 4-byte
- * aligned.  B = 0 is a no-op returning BI_OK.  Limits: max_pages * page_size < 2^31, B * num_heads * chunks < 2^31.
+ * aligned.  B = 0 is a no-op returning BI_OK.  Limits: B <= 16384, max_pages * page_size <= 2^30, and at most
+ * 2^30 partial results (B * num_heads * chunks, with at most 128 chunks).
  * Errors: BI_ERR_INVALID_ARG, BI_ERR_ALIGNMENT, BI_ERR_UNSUPPORTED_SHAPE, BI_ERR_NO_DEVICE,
  * BI_ERR_CUDA.
  */

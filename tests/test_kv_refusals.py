@@ -69,7 +69,7 @@ def test_block_tables(change, status):
     ({"B": -1}, BAD), ({"Hq": 0}, BAD), ({"max_pages": -1}, BAD), ({"ld_table": 3}, BAD), ({"window": -1}, BAD),
     ({"ldq": 1016}, BAD), ({"ldo": 8}, BAD), ({"scale": float("nan")}, BAD), ({"scale": float("inf")}, BAD),
     ({"Hq": 7, "ldq": 4096}, SHAPE), ({"Hq": 34, "ldq": 8192, "ldo": 8192}, SHAPE), ({"max_pages": 2 ** 27, "ld_table": 2 ** 27}, SHAPE),
-    ({"B": 2 ** 31}, SHAPE), ({"ldq": 2 ** 60}, SHAPE), ({"Q": None}, BAD), ({"table": None}, BAD), ({"lens": None}, BAD),
+    ({"B": 2 ** 31}, SHAPE), ({"B": 16385}, SHAPE), ({"max_pages": 2 ** 26 + 1, "ld_table": 2 ** 27}, SHAPE), ({"ldq": 2 ** 60}, SHAPE), ({"Q": None}, BAD), ({"table": None}, BAD), ({"lens": None}, BAD),
     ({"O": None}, BAD), ({"Q": 264}, ALIGN), ({"O": 264}, ALIGN), ({"ldq": 1028}, ALIGN), ({"ldo": 1028}, ALIGN),
     ({"table": 258}, ALIGN), ({"lens": 257}, ALIGN), ({"lse": 258}, ALIGN), ({"B": 0, "Q": None, "O": None}, 0)])
 def test_attention(change, status):

@@ -59,11 +59,12 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kWeightExp = 15.0f;         // weights are held times 2^15
 
-// Steps per chunk of a sequence of `steps` steps.  Few chunks keep the partial results small (one
-// is 1/32 of the bytes of a step with 4 query heads), many spread a long sequence over the CTAs.
+// Steps per chunk of a sequence of `steps` steps.  Opening and closing a chunk costs about as much as
+// one step, so chunks grow with the sequence; short sequences keep one-step chunks, which spread a
+// single request over more CTAs, and no sequence has more than kMaxChunks.
 __host__ __device__ __forceinline__ int chunk_steps(int steps)
 {
-    int s = 1;
+    int s = steps <= 4 ? 1 : steps <= 16 ? 2 : 4;
     while (s * kMaxChunks < steps)
         s *= 2;
     return s;
@@ -105,7 +106,7 @@ __device__ __forceinline__ Span span_of(int len, const AttnArgs &a)
 }
 
 // One warp's tile.
-enum : int { kFirst = 1, kLast = 2, kEnd = 4, kBad = 8, kHalf0 = 16, kHalf1 = 32 };
+enum : int { kFirst = 1, kLast = 2, kEnd = 4, kBad = 8, kHalf0 = 16, kHalf1 = 32, kWhole = 64 };
 struct Desc {
     int b, kvh, key0, lo, hi, flags, chunk, chunks;
 };
@@ -167,6 +168,18 @@ __device__ __forceinline__ float exp2_approx(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float log2_approx(float x)
+{
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_approx(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi)
 {
     const __half2 h = __floats2half2_rn(lo, hi);
@@ -217,6 +230,8 @@ __device__ __forceinline__ int out_offset(int head, int d)
 // Walks the items of this CTA and the steps of each, giving one warp's tiles in order.
 struct Cursor {
     int item, items, stride;   // item = chunk ordinal * heads + key/value head
+    int u, du, dh;             // chunk ordinal; the stride's quotient and remainder by the heads
+    const int32_t *pages;      // the sequence's row of the block table
     int step, steps;           // of the current chunk
     Desc d;
     int chunk_key;             // the chunk's first position
@@ -231,8 +246,7 @@ __device__ __forceinline__ int len_of(const AttnArgs &a, const int32_t *len_s, i
 __device__ __forceinline__ void open_item(Cursor &c, const AttnArgs &a, const int32_t *first_chunk, const int32_t *len_s)
 {
     const int lane = threadIdx.x & 31;
-    const int u = c.item / a.heads;
-    c.d.kvh = c.item - u * a.heads;
+    const int u = c.u;
     // the last entry with first_chunk <= u: 16 entries a lane, then one
     const int blk = __popc(__ballot_sync(kFull, first_chunk[lane * 16] <= u)) - 1;
     const int e = blk * 16 + __popc(__ballot_sync(kFull, lane < 16 && first_chunk[blk * 16 + lane] <= u)) - 1;
@@ -265,6 +279,7 @@ __device__ __forceinline__ void open_item(Cursor &c, const AttnArgs &a, const in
     c.d.chunk = chunk;
     c.d.chunks = s.chunks;
     c.d.flags = s.bad ? kBad : 0;
+    c.pages = a.table + b * a.ld_table;
     c.step = 0;
     c.steps = min(s.per_chunk, s.steps - chunk * s.per_chunk);
     c.chunk_key = (s.first + chunk * s.per_chunk) * kStep;
@@ -279,11 +294,18 @@ __device__ __forceinline__ Desc next_tile(Cursor &c, const AttnArgs &a, const in
         return d;
     }
     d.key0 = c.chunk_key + c.step * kStep + static_cast<int>(threadIdx.x >> 5) * kTile;
+    d.flags |= d.key0 >= d.lo && d.key0 + kTile <= d.hi ? kWhole : 0;
     d.flags |= (c.step == 0 ? kFirst : 0) | (c.step == c.steps - 1 ? kLast : 0);
     d.flags |= (d.key0 < d.hi && d.key0 + kTile / 2 > d.lo ? kHalf0 : 0) |
                (d.key0 + kTile / 2 < d.hi && d.key0 + kTile > d.lo ? kHalf1 : 0);
     if (++c.step == c.steps) {
         c.item += c.stride;
+        c.u += c.du;
+        c.d.kvh += c.dh;
+        if (c.d.kvh >= a.heads) {
+            c.d.kvh -= a.heads;
+            ++c.u;
+        }
         if (c.item < c.items)
             open_item(c, a, first_chunk, len_s);
     }
@@ -353,21 +375,30 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
     cur.item = blockIdx.x;
     cur.items = total * a.heads;
     cur.stride = gridDim.x;
+    cur.u = cur.item / a.heads;
+    cur.d.kvh = cur.item - cur.u * a.heads;
+    cur.du = cur.stride / a.heads;
+    cur.dh = cur.stride - cur.du * a.heads;
     if (cur.item >= cur.items)
         return;
     open_item(cur, a, sm.first_chunk, sm.len);
 
     // tile i: descriptor and page numbers
     auto ask_pages = [&](int i) {
+        const int32_t *pages = cur.pages;
         const Desc d = next_tile(cur, a, sm.first_chunk, sm.len);
         if (lane < 2) {
             reinterpret_cast<int4 *>(&sm.desc[warp][i % kDescs])[lane] =
                 lane == 0 ? make_int4(d.b, d.kvh, d.key0, d.lo) : make_int4(d.hi, d.flags, d.chunk, d.chunks);
             if (d.flags & (lane == 0 ? kHalf0 : kHalf1))
                 copy4(smem_u32(&sm.page[warp][i % kDescs][lane]),
-                      a.table + d.b * a.ld_table + ((d.key0 + lane * (kTile / 2)) >> a.page_shift));
+                      pages + ((d.key0 + lane * (kTile / 2)) >> a.page_shift));
         }
     };
+    // this lane's 16-byte group and first row of a tile, in the cache and in shared memory
+    const int grp = lane % kGroups, row0 = lane / kGroups;
+    const int64_t lane_at = row0 * a.token_stride + grp * 16, row_step = kRows * a.token_stride;
+    const uint32_t lane_dst = tile_offset<D>(row0, grp);
     // tile i: codes and scales, its page numbers having come
     auto ask_codes = [&](int i) {
         const Desc d = sm.desc[warp][i % kDescs];
@@ -393,17 +424,28 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
                     *dst = in ? NAN : 1.0f;     // a page number out of range
             }
         }
-        const int grp = lane % kGroups, row0 = lane / kGroups;
         const uint32_t dst = smem_u32(&sm.ring[warp][stage][0][0]);
+        if ((d.flags & kWhole) && ok[0] && ok[1]) {
+            // 16 rows of each half; the swizzle of rows kRows apart repeats after one or two of them
+            const int64_t from[2] = {base[0] + lane_at, base[1] + lane_at};
+#pragma unroll
+            for (int r = 0; r < kTile; r += kRows) {
+                const int64_t at = from[r / (kTile / 2)] + (r % (kTile / 2)) / kRows * row_step;
+                const uint32_t off = dst + r * D + (D == 128 && (r & 4) ? lane_dst ^ 64 : lane_dst);
+                copy16(off, a.k + at, true);
+                copy16(off + S::kMatrix, a.v + at, true);
+            }
+            return;
+        }
 #pragma unroll
         for (int r = 0; r < kTile; r += kRows) {
             const int row = r + row0, h = r >= kTile / 2 ? 1 : 0;
             const int key = d.key0 + row;
             const bool valid = ok[h] && key >= d.lo && key < d.hi;
-            const int64_t at = valid ? base[h] + (row & (kTile / 2 - 1)) * a.token_stride + grp * 16 : 0;
-            const int off = tile_offset<D>(row, grp);
-            copy16(dst + off, a.k + at, valid);
-            copy16(dst + S::kMatrix + off, a.v + at, valid);
+            const int64_t at = valid ? base[h] + lane_at + (r % (kTile / 2)) / kRows * row_step : 0;
+            const uint32_t off = dst + tile_offset<D>(row, grp);
+            copy16(off, a.k + at, valid);
+            copy16(off + S::kMatrix, a.v + at, valid);
         }
     };
     // the queries of tile i's item (item number n of this CTA): this warp's share
@@ -533,21 +575,36 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
             // base-2 exponents t_j, and their maximum
             const float sk[2] = {checked_scale(sc.x), checked_scale(sc.y)};
             const float sv[2] = {checked_scale(sc.z), checked_scale(sc.w)};
-            const float lsv[2] = {log2f(sv[0]), log2f(sv[1])};
-            const float rsv[2] = {1.0f / sv[0], 1.0f / sv[1]};
+            // approximate to 2^-22: a page's weights are all off by the same factor, less than 2^-21
+            const float lsv[2] = {log2_approx(sv[0]), log2_approx(sv[1])};
+            const float rsv[2] = {rcp_approx(sv[0]), rcp_approx(sv[1])};
+            const bool whole = (d.flags & kWhole) != 0;
             uint32_t pf[NT][2][2];    // weights as the second operand: [tile of 16][keys 0-7, 8-15]
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 float mx[2] = {m[n][0], m[n][1]};
 #pragma unroll
+                for (int mt = 0; mt < 2; ++mt) {
+                    const float c[2] = {qc[n][0] * sk[mt], qc[n][1] * sk[mt]};
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        s[n][mt][x] = fmaf(s[n][mt][x], c[x & 1], lsv[mt]);
+                }
+                if (!whole) {
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const int key = d.key0 + mt * 16 + g + (x >> 1) * 8;
+                            if (key < d.lo || key >= d.hi)
+                                s[n][mt][x] = -INFINITY;
+                        }
+                }
+#pragma unroll
                 for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int key = d.key0 + mt * 16 + g + (x >> 1) * 8;
-                        const float v = fmaf(s[n][mt][x], qc[n][x & 1] * sk[mt], lsv[mt]);
-                        s[n][mt][x] = key >= d.lo && key < d.hi ? v : -INFINITY;
+                    for (int x = 0; x < 4; ++x)
                         mx[x & 1] = fmaxf(mx[x & 1], s[n][mt][x]);
-                    }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     mx[h] = fmaxf(mx[h], __shfl_xor_sync(kFull, mx[h], 4));
@@ -555,12 +612,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
                     mx[h] = fmaxf(mx[h], __shfl_xor_sync(kFull, mx[h], 16));
                 }
                 const float corr[2] = {exp2_approx(m[n][0] - mx[0]), exp2_approx(m[n][1] - mx[1])};
+                const float ref[2] = {mx[0] - kWeightExp, mx[1] - kWeightExp};
                 float sum[2] = {0.0f, 0.0f};
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt) {
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        s[n][mt][x] = exp2_approx(s[n][mt][x] - mx[x & 1] + kWeightExp);
+                        s[n][mt][x] = exp2_approx(s[n][mt][x] - ref[x & 1]);
                         sum[x & 1] = fmaf(s[n][mt][x], rsv[mt], sum[x & 1]);
                     }
                     pf[n][mt][0] = transpose8x8(pack_half(s[n][mt][0], s[n][mt][1]));

@@ -6,14 +6,17 @@
 //
 // Work.  A sequence's positions are cut into steps of 256 at multiples of 256, and runs of steps
 // into chunks whose length follows from the number of steps alone.  An item is one chunk of one
-// key/value head; persistent CTAs take items round robin.  Warp w of a CTA owns positions
+// key/value head; persistent CTAs take items round robin.  Consumer warp w of a CTA owns positions
 // 32 w .. 32 w + 31 of every step and keeps a softmax state of its own over the chunk; the eight
 // states are added in warp order at the chunk's end, and the chunks in ascending order by a second
 // kernel.  Every sum's order is thus fixed by the sequence's length and window.
 //
-// Loads.  Each warp streams its own tiles through a private ring of stages with cp.async: rows
-// outside the sequence are filled with zeros (so a stale NaN code cannot reach a sum through a
-// zero weight); page numbers come twice as many tiles ahead as codes.  No CTA-wide hand-off.
+// Roles (16 warps, one CTA per SM).  Four producer warps stream half-steps of 128 positions into a
+// ring of stages, one tile of 32 positions each, with cp.async: rows outside the sequence are
+// filled with zeros, so a stale NaN code cannot reach a sum through a zero weight.  Eight consumer
+// warps do nothing but the matrix products and the softmax.  Four helper warps prepare the next
+// items' queries and add the states of the chunks that are done.  (With the three jobs in every
+// warp, a tile took 964 warp instructions, 149 us for 64 sequences of 4096 positions, 32/8 heads.)
 //
 // Matrix products.  The cache is the first operand of mma.m16n8k16 (16 positions, or 16 dimensions,
 // a time) and the query heads are the 8 columns, so grouped queries fill the tile instead of
@@ -41,23 +44,30 @@
 
 #include "bi_kv_common.cuh"
 #include "bi_paged_attention.h"
+#include "ptx_sm100.cuh"
 
 namespace {
 
 using bi_kv::kFull;
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
+constexpr int kConsumers = 8;               // warps, as for the next two
+constexpr int kHelpers = 4;
+constexpr int kProducers = 4;
+constexpr int kThreads = 32 * (kConsumers + kHelpers + kProducers);
 constexpr int kTile = 32;                   // positions of a warp's tile
-constexpr int kStep = kWarps * kTile;       // positions of a CTA's step
+constexpr int kHalf = kProducers * kTile;   // positions of a stage: half a step
+constexpr int kStep = kConsumers * kTile;   // positions of a CTA's step
 constexpr int kMaxChunks = 128;             // chunks of a sequence
 constexpr int kMaxGroup = 16;               // query heads of a key/value head
 constexpr int kEntries = 512;               // entries of the scanned chunk counts
 constexpr int kMaxBatch = kEntries * 32;    // an entry stands for up to 32 sequences
-constexpr int kDescs = 16;                  // ring of tile descriptors
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kWeightExp = 15.0f;         // weights are held times 2^15
+// A wait on a stage that lasts this many SM cycles (a second) gives up; every later wait of the CTA
+// then returns at once and its outputs are NaN.
+constexpr uint64_t kWaitCycles = UINT64_C(2000000000);
+static_assert(kStep == 2 * kHalf, "a step is two stages");
 
 // Steps per chunk of a sequence of `steps` steps.  Opening and closing a chunk costs about as much as
 // one step, so chunks grow with the sequence; short sequences keep one-step chunks, which spread a
@@ -105,13 +115,6 @@ __device__ __forceinline__ Span span_of(int len, const AttnArgs &a)
     return s;
 }
 
-// One warp's tile.
-enum : int { kFirst = 1, kLast = 2, kEnd = 4, kBad = 8, kHalf0 = 16, kHalf1 = 32, kWhole = 64 };
-struct Desc {
-    int b, kvh, key0, lo, hi, flags, chunk, chunks;
-};
-static_assert(sizeof(Desc) == 32, "two 16-byte words");
-
 // ---------------------------------------------------------------------------------------------
 // instructions
 // ---------------------------------------------------------------------------------------------
@@ -128,9 +131,7 @@ __device__ __forceinline__ void copy4(uint32_t dst, const void *src)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr)
 {
@@ -194,21 +195,34 @@ __device__ __forceinline__ float checked_scale(float s) { return s >= 0x1p-64f &
 // shared memory
 // ---------------------------------------------------------------------------------------------
 
+enum : int { kFirst = 1, kLast = 2, kEnd = 4 };
+
+// What a stage holds: positions key0 .. key0 + 127, of which [lo, hi) count.
+struct Stage {
+    int key0, lo, hi, flags;
+};
+
 template <int D, int NT>
 struct Shared {
-    static constexpr int kStages = D == 128 ? 3 : 6;
-    static constexpr int kAhead = kStages - 1;              // tiles of codes in flight
-    static constexpr int kQueries = kAhead + 2;             // items whose queries are held
+    static constexpr int kCols = NT * 8;
+    // 32 KB stages of D = 128 (16 KB of D = 64) beside the chunk states, 192 KB together at most
+    static constexpr int kStages = D == 128 ? (NT == 1 ? 5 : 4) : 8;
     static constexpr int kMatrix = kTile * D;               // bytes of a tile's keys (or values)
-    uint8_t ring[kWarps][kStages][2][kMatrix];              // codes; at a chunk's end a warp's outputs
-    alignas(16) __nv_bfloat16 q[kQueries][NT * 8][D];
-    float4 scale[kWarps][kStages];                          // key scales of the halves, value scales
-    Desc desc[kWarps][kDescs];
-    int32_t page[kWarps][kDescs][2];                    // page numbers of a tile's halves
-    float2 ml[kWarps][NT * 8];
+    uint8_t ring[kStages][kProducers][2][kMatrix];
+    float state[kConsumers][kCols][D];                      // a chunk's outputs, not normalised
+    uint4 q[2][NT][D / 32][32];                             // two items' queries, as the consumers' lanes hold them
+    float4 scale[kStages][kProducers];                      // of a tile's two 16s: key scales, value scales
+    Stage stage[kStages];
+    float2 ml[kConsumers][kCols];                           // a chunk's maxima and sums
+    float qc[2][kCols];                                     // scale * log2 e * the power of two taken out
+    uint64_t full[kStages], empty[kStages];                 // a stage is filled, is consumed
+    // A chunk's states are written; the helpers have read the states of the item before and prepared
+    // the queries of the one after (even and odd items apart: the helpers may be one ahead).
+    uint64_t states, helped[2];
     int32_t first_chunk[kEntries + 32];                     // chunks before each entry
     int32_t len[kEntries];                                  // lengths, when an entry is one sequence
-    int32_t warp_sum[kWarps];
+    int32_t warp_sum[kThreads / 32];
+    int dead;                                               // a wait gave up
 };
 
 // Byte of the 16-byte group `grp` of row `row` inside a tile: groups are spread over the banks so
@@ -219,38 +233,53 @@ __device__ __forceinline__ int tile_offset(int row, int grp)
     return row * D + ((D == 128 ? grp ^ (row & 7) : grp ^ ((row >> 1) & 3)) << 4);
 }
 
-// Float of dimension d (even) of column `head` inside a warp's outputs: the columns 2t of a quad
-// fall on different banks.
+// Float of dimension d (even) of column `head` inside a state: the columns 2t of a quad fall on
+// different banks.
 template <int D>
-__device__ __forceinline__ int out_offset(int head, int d)
+__device__ __forceinline__ int state_offset(int head, int d)
 {
     return head * D + (d ^ (((head >> 1) & 3) << 3));
 }
 
-// Walks the items of this CTA and the steps of each, giving one warp's tiles in order.
-struct Cursor {
-    int item, items, stride;   // item = chunk ordinal * heads + key/value head
-    int u, du, dh;             // chunk ordinal; the stride's quotient and remainder by the heads
-    const int32_t *pages;      // the sequence's row of the block table
-    int step, steps;           // of the current chunk
-    Desc d;
-    int chunk_key;             // the chunk's first position
-};
-
-__device__ __forceinline__ int len_of(const AttnArgs &a, const int32_t *len_s, int b)
+template <typename S>
+__device__ __forceinline__ void wait_for(S &sm, uint64_t *bar, uint32_t parity)
 {
-    return a.b <= kEntries ? len_s[b] : a.lens[b];
+    if (!bi::ptx::mbar_wait(bar, parity, kWaitCycles, &sm.dead))
+        *static_cast<volatile int *>(&sm.dead) = 1;
 }
 
-// The sequence and chunk of chunk ordinal u (all lanes alike).
-__device__ __forceinline__ void open_item(Cursor &c, const AttnArgs &a, const int32_t *first_chunk, const int32_t *len_s)
+// One arrival of this warp, which releases what all of it has written.
+__device__ __forceinline__ void warp_arrive(uint64_t *bar)
+{
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+        bi::ptx::mbar_arrive(bar);
+}
+
+// One arrival on `bar` once every cp.async of this thread so far has landed.
+__device__ __forceinline__ void arrive_after_copies(uint64_t *bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Walks the items of this CTA, one chunk of one key/value head each.
+struct Items {
+    int item, items, stride;   // item = chunk ordinal * heads + key/value head
+    int u, du, dh;             // chunk ordinal; the stride's quotient and remainder by the heads
+    int b, kvh, lo, hi, chunk, chunks, steps, key0;
+    bool bad;
+
+    __device__ __forceinline__ bool done() const { return item >= items; }
+};
+
+// The sequence and chunk of chunk ordinal it.u (all lanes alike).
+__device__ __forceinline__ void open_item(Items &it, const AttnArgs &a, const int32_t *first_chunk, const int32_t *len_s)
 {
     const int lane = threadIdx.x & 31;
-    const int u = c.u;
     // the last entry with first_chunk <= u: 16 entries a lane, then one
-    const int blk = __popc(__ballot_sync(kFull, first_chunk[lane * 16] <= u)) - 1;
-    const int e = blk * 16 + __popc(__ballot_sync(kFull, lane < 16 && first_chunk[blk * 16 + lane] <= u)) - 1;
-    int chunk = u - first_chunk[e], b = e;
+    const int blk = __popc(__ballot_sync(kFull, first_chunk[lane * 16] <= it.u)) - 1;
+    const int e = blk * 16 + __popc(__ballot_sync(kFull, lane < 16 && first_chunk[blk * 16 + (lane & 15)] <= it.u)) - 1;
+    int chunk = it.u - first_chunk[e], b = e;
     Span s;
     if (a.b <= kEntries) {
         s = span_of(len_s[b], a);
@@ -260,8 +289,8 @@ __device__ __forceinline__ void open_item(Cursor &c, const AttnArgs &a, const in
         const int mine = e * per + lane;
         const bool own = lane < per && mine < a.b;
         const Span x = span_of(own ? a.lens[mine] : 0, a);
-        int incl = own ? x.chunks : 0;
-        const int n = incl;
+        const int n = own ? x.chunks : 0;
+        int incl = n;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int y = __shfl_up_sync(kFull, incl, off);
@@ -273,266 +302,162 @@ __device__ __forceinline__ void open_item(Cursor &c, const AttnArgs &a, const in
         b = e * per + at;
         s = span_of(a.lens[b], a);
     }
-    c.d.b = b;
-    c.d.lo = s.lo;
-    c.d.hi = s.hi;
-    c.d.chunk = chunk;
-    c.d.chunks = s.chunks;
-    c.d.flags = s.bad ? kBad : 0;
-    c.pages = a.table + b * a.ld_table;
-    c.step = 0;
-    c.steps = min(s.per_chunk, s.steps - chunk * s.per_chunk);
-    c.chunk_key = (s.first + chunk * s.per_chunk) * kStep;
+    it.b = b;
+    it.lo = s.lo;
+    it.hi = s.hi;
+    it.bad = s.bad;
+    it.chunk = chunk;
+    it.chunks = s.chunks;
+    it.steps = min(s.per_chunk, s.steps - chunk * s.per_chunk);
+    it.key0 = (s.first + chunk * s.per_chunk) * kStep;
 }
 
-// The cursor's tile, then one tile on.
-__device__ __forceinline__ Desc next_tile(Cursor &c, const AttnArgs &a, const int32_t *first_chunk, const int32_t *len_s)
+__device__ __forceinline__ void next_item(Items &it, const AttnArgs &a, const int32_t *first_chunk, const int32_t *len_s)
 {
-    Desc d = c.d;
-    if (c.item >= c.items) {
-        d.flags = kEnd;
-        return d;
+    it.item += it.stride;
+    it.u += it.du;
+    it.kvh += it.dh;
+    if (it.kvh >= a.heads) {
+        it.kvh -= a.heads;
+        ++it.u;
     }
-    d.key0 = c.chunk_key + c.step * kStep + static_cast<int>(threadIdx.x >> 5) * kTile;
-    d.flags |= d.key0 >= d.lo && d.key0 + kTile <= d.hi ? kWhole : 0;
-    d.flags |= (c.step == 0 ? kFirst : 0) | (c.step == c.steps - 1 ? kLast : 0);
-    d.flags |= (d.key0 < d.hi && d.key0 + kTile / 2 > d.lo ? kHalf0 : 0) |
-               (d.key0 + kTile / 2 < d.hi && d.key0 + kTile > d.lo ? kHalf1 : 0);
-    if (++c.step == c.steps) {
-        c.item += c.stride;
-        c.u += c.du;
-        c.d.kvh += c.dh;
-        if (c.d.kvh >= a.heads) {
-            c.d.kvh -= a.heads;
-            ++c.u;
-        }
-        if (c.item < c.items)
-            open_item(c, a, first_chunk, len_s);
-    }
-    return d;
+    if (!it.done())
+        open_item(it, a, first_chunk, len_s);
 }
 
+// ---------------------------------------------------------------------------------------------
+// the roles
+// ---------------------------------------------------------------------------------------------
+
+// Producer warp p copies tile p of every stage.
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __grid_constant__ AttnArgs a)
+__device__ __forceinline__ void produce(Shared<D, NT> &sm, const AttnArgs &a, Items it, int p)
 {
     using S = Shared<D, NT>;
-    constexpr int kCols = NT * 8;
-    constexpr int kGroups = D / 16;                 // 16-byte groups of a row
-    constexpr int kRows = 32 / kGroups;             // rows one load instruction of a warp covers
-    constexpr int kQueries = S::kQueries;
-    // page numbers are asked for kIds tiles ahead: the copies of that many less kAhead tiles ago, whose
-    // group they are in, have been waited for when the codes are
-    constexpr int kIds = 2 * S::kAhead;
-    static_assert(kIds + 1 <= kDescs && (kDescs & (kDescs - 1)) == 0, "live descriptors");
-    static_assert(kCols * D * 4 <= 2 * S::kMatrix, "a warp's outputs fit in a stage");
-    extern __shared__ __align__(128) uint8_t smem_raw[];
-    S &sm = *reinterpret_cast<S *>(smem_raw);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int g = lane >> 2, t = lane & 3;
-    bi_kv::dependency_wait();
-
-    // chunks before each entry: thread i scans entries 2i and 2i + 1
-    {
-        const int per = (a.b + kEntries - 1) / kEntries;
-        int n[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int e = 2 * tid + j;
-            n[j] = 0;
-            for (int b = e * per; b < (e + 1) * per && b < a.b; ++b) {
-                const int len = a.lens[b];
-                if (per == 1)
-                    sm.len[e] = len;
-                n[j] += span_of(len, a).chunks;
-            }
-        }
-        int incl = n[0] + n[1];
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int y = __shfl_up_sync(kFull, incl, off);
-            if (lane >= off)
-                incl += y;
-        }
-        if (lane == 31)
-            sm.warp_sum[warp] = incl;
-        __syncthreads();
-        int before = 0;
-        for (int w = 0; w < warp; ++w)
-            before += sm.warp_sum[w];
-        // entries behind the last sequence hold INT_MAX but the first of them, which ends the scan
-        const int base = before + incl - n[0] - n[1];
-        const int last = (a.b + per - 1) / per;
-        sm.first_chunk[2 * tid] = 2 * tid <= last ? base : INT_MAX;
-        sm.first_chunk[2 * tid + 1] = 2 * tid + 1 <= last ? base + n[0] : INT_MAX;
-        if (tid < 32)
-            sm.first_chunk[kEntries + tid] = INT_MAX;
-        __syncthreads();
-    }
-    int total = 0;
-    for (int w = 0; w < kWarps; ++w)
-        total += sm.warp_sum[w];
-    Cursor cur;
-    cur.item = blockIdx.x;
-    cur.items = total * a.heads;
-    cur.stride = gridDim.x;
-    cur.u = cur.item / a.heads;
-    cur.d.kvh = cur.item - cur.u * a.heads;
-    cur.du = cur.stride / a.heads;
-    cur.dh = cur.stride - cur.du * a.heads;
-    if (cur.item >= cur.items)
-        return;
-    open_item(cur, a, sm.first_chunk, sm.len);
-
-    // tile i: descriptor and page numbers
-    auto ask_pages = [&](int i) {
-        const int32_t *pages = cur.pages;
-        const Desc d = next_tile(cur, a, sm.first_chunk, sm.len);
-        if (lane < 2) {
-            reinterpret_cast<int4 *>(&sm.desc[warp][i % kDescs])[lane] =
-                lane == 0 ? make_int4(d.b, d.kvh, d.key0, d.lo) : make_int4(d.hi, d.flags, d.chunk, d.chunks);
-            if (d.flags & (lane == 0 ? kHalf0 : kHalf1))
-                copy4(smem_u32(&sm.page[warp][i % kDescs][lane]),
-                      pages + ((d.key0 + lane * (kTile / 2)) >> a.page_shift));
-        }
-    };
-    // this lane's 16-byte group and first row of a tile, in the cache and in shared memory
+    constexpr int kGroups = D / 16;        // 16-byte groups of a row
+    constexpr int kRows = 32 / kGroups;    // rows one copy instruction covers
+    const int lane = threadIdx.x & 31;
+    const int page_mask = (1 << a.page_shift) - 1;
+    // this lane's 16-byte group and first row, in the cache and in shared memory
     const int grp = lane % kGroups, row0 = lane / kGroups;
     const int64_t lane_at = row0 * a.token_stride + grp * 16, row_step = kRows * a.token_stride;
     const uint32_t lane_dst = tile_offset<D>(row0, grp);
-    // tile i: codes and scales, its page numbers having come
-    auto ask_codes = [&](int i) {
-        const Desc d = sm.desc[warp][i % kDescs];
-        if (!(d.flags & (kHalf0 | kHalf1)))
-            return;
-        const int stage = i % S::kStages;
-        const int page_mask = (1 << a.page_shift) - 1;
-        int64_t base[2];
-        bool ok[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int id = sm.page[warp][i % kDescs][h];
-            const bool in = (d.flags & (h == 0 ? kHalf0 : kHalf1)) != 0;
-            ok[h] = in && id >= 0 && id < a.num_pages;
-            base[h] = ok[h] ? id * a.page_stride + ((d.key0 + h * (kTile / 2)) & page_mask) * a.token_stride +
-                                  d.kvh * a.head_stride
-                            : 0;
-            if (lane == h || lane == h + 2) {   // lanes 0, 1: key scales, 2, 3: value scales
-                float *dst = reinterpret_cast<float *>(&sm.scale[warp][stage]) + lane;
-                if (ok[h])
-                    copy4(smem_u32(dst), (lane < 2 ? a.k_scale : a.v_scale) + static_cast<int64_t>(id) * a.heads + d.kvh);
-                else
-                    *dst = in ? NAN : 1.0f;     // a page number out of range
-            }
-        }
-        const uint32_t dst = smem_u32(&sm.ring[warp][stage][0][0]);
-        if ((d.flags & kWhole) && ok[0] && ok[1]) {
-            // 16 rows of each half; the swizzle of rows kRows apart repeats after one or two of them
-            const int64_t from[2] = {base[0] + lane_at, base[1] + lane_at};
-#pragma unroll
-            for (int r = 0; r < kTile; r += kRows) {
-                const int64_t at = from[r / (kTile / 2)] + (r % (kTile / 2)) / kRows * row_step;
-                const uint32_t off = dst + r * D + (D == 128 && (r & 4) ? lane_dst ^ 64 : lane_dst);
-                copy16(off, a.k + at, true);
-                copy16(off + S::kMatrix, a.v + at, true);
-            }
-            return;
-        }
-#pragma unroll
-        for (int r = 0; r < kTile; r += kRows) {
-            const int row = r + row0, h = r >= kTile / 2 ? 1 : 0;
-            const int key = d.key0 + row;
-            const bool valid = ok[h] && key >= d.lo && key < d.hi;
-            const int64_t at = valid ? base[h] + lane_at + (r % (kTile / 2)) / kRows * row_step : 0;
-            const uint32_t off = dst + tile_offset<D>(row, grp);
-            copy16(off, a.k + at, valid);
-            copy16(off + S::kMatrix, a.v + at, valid);
-        }
-    };
-    // the queries of tile i's item (item number n of this CTA): this warp's share
-    auto ask_queries = [&](int i, int n) {
-        const Desc d = sm.desc[warp][i % kDescs];
-        const int vecs = a.group * (D / 8);
-        const __nv_bfloat16 *src = a.q + d.b * a.ldq + static_cast<int64_t>(d.kvh) * a.group * D;
-        for (int x = warp * 32 + lane; x < vecs; x += kThreads)
-            copy16(smem_u32(&sm.q[n % kQueries][0][0]) + x * 16, src + x * 8, true);
-    };
 
-    // Queries run one tile further ahead than codes: the barrier at the end of the item before
-    // makes the other warps' shares visible.
-    for (int i = 0; i < kIds; ++i)
-        ask_pages(i);
-    copy_commit();
-    copy_wait<0>();
-    __syncwarp();
-    int asked_items = 0;
-#pragma unroll
-    for (int i = 0; i < S::kAhead; ++i) {
-        ask_codes(i);
-        if (i == 0)   // the queries of the items that open in the first kAhead + 1 tiles
-            for (int j = 0; j <= S::kAhead; ++j) {
-                const int flags = sm.desc[warp][j].flags;
-                if ((flags & kFirst) && !(flags & kEnd))
-                    ask_queries(j, asked_items++);
-            }
-        copy_commit();
-    }
-    // zero columns of the query ring that no head fills, once
-    for (int x = tid; x < kQueries * (kCols - a.group) * (D / 2); x += kThreads) {
-        const int per = (kCols - a.group) * (D / 2);
-        reinterpret_cast<uint32_t *>(&sm.q[x / per][a.group][0])[x % per] = 0;
-    }
-    copy_wait<S::kAhead - 1>();
-    __syncthreads();
+    // lanes 0 and 1 hold the page numbers of the tile's first and second 16 positions
+    auto page_of = [&](const Items &x, int key0) {
+        const int key = key0 + p * kTile + lane * (kTile / 2);
+        return !x.done() && lane < 2 && key < x.hi && key + kTile / 2 > x.lo
+                   ? a.table[x.b * a.ld_table + (key >> a.page_shift)]
+                   : -1;
+    };
+    int slot = 0;
+    uint32_t parity = 1;     // of a stage not used yet
+    int half = 0;            // of the current item
+    int mine = page_of(it, it.key0);
+    while (true) {
+        const bool end = it.done();
+        const int key0 = it.key0 + half * kHalf;
+        const int kvh = it.kvh;
+        const Stage st = {key0, it.lo, it.hi,
+                          end ? kEnd : (half < 2 ? kFirst : 0) | (half >= 2 * it.steps - 2 ? kLast : 0)};
+        const int id[2] = {__shfl_sync(kFull, mine, 0), __shfl_sync(kFull, mine, 1)};
+        // the next stage's page numbers come while this one waits for its place
+        if (++half == (end ? 2 : 2 * it.steps) && !end) {
+            half = 0;
+            next_item(it, a, sm.first_chunk, sm.len);
+        }
+        mine = page_of(it, it.key0 + half * kHalf);
 
+        wait_for(sm, &sm.empty[slot], parity);
+        if (p == 0 && lane == 0)
+            sm.stage[slot] = st;
+        const int tile0 = key0 + p * kTile;
+        if (!end && tile0 < st.hi && tile0 + kTile > st.lo) {
+            int64_t base[2];
+            bool ok[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int key = tile0 + h * (kTile / 2);
+                const bool in = key < st.hi && key + kTile / 2 > st.lo;
+                ok[h] = in && id[h] >= 0 && id[h] < a.num_pages;
+                base[h] = ok[h] ? id[h] * a.page_stride + (key & page_mask) * a.token_stride + kvh * a.head_stride : 0;
+                if (lane == h || lane == h + 2) {   // lanes 0, 1: key scales, 2, 3: value scales
+                    float *dst = reinterpret_cast<float *>(&sm.scale[slot][p]) + lane;
+                    if (ok[h])
+                        copy4(smem_u32(dst), (lane < 2 ? a.k_scale : a.v_scale) + static_cast<int64_t>(id[h]) * a.heads + kvh);
+                    else
+                        *dst = in ? NAN : 1.0f;     // a page number out of range
+                }
+            }
+            const uint32_t dst = smem_u32(&sm.ring[slot][p][0][0]);
+            if (ok[0] && ok[1] && tile0 >= st.lo && tile0 + kTile <= st.hi) {
+                // whole; the swizzle of rows kRows apart repeats after one or two of them
+                const int64_t from[2] = {base[0] + lane_at, base[1] + lane_at};
+#pragma unroll
+                for (int r = 0; r < kTile; r += kRows) {
+                    const int64_t at = from[r / (kTile / 2)] + (r % (kTile / 2)) / kRows * row_step;
+                    const uint32_t off = dst + r * D + (D == 128 && (r & 4) ? lane_dst ^ 64 : lane_dst);
+                    copy16(off, a.k + at, true);
+                    copy16(off + S::kMatrix, a.v + at, true);
+                }
+            } else {
+#pragma unroll
+                for (int r = 0; r < kTile; r += kRows) {
+                    const int row = r + row0, h = r / (kTile / 2);
+                    const int key = tile0 + row;
+                    const bool valid = ok[h] && key >= st.lo && key < st.hi;
+                    const int64_t at = valid ? base[h] + lane_at + (r % (kTile / 2)) / kRows * row_step : 0;
+                    const uint32_t off = dst + tile_offset<D>(row, grp);
+                    copy16(off, a.k + at, valid);
+                    copy16(off + S::kMatrix, a.v + at, valid);
+                }
+            }
+        }
+        arrive_after_copies(&sm.full[slot]);
+        warp_arrive(&sm.full[slot]);   // releases the words stored above
+        if (++slot == S::kStages) {
+            slot = 0;
+            parity ^= 1;
+        }
+        if ((end && half == 2) || *static_cast<volatile int *>(&sm.dead))
+            break;
+    }
+    copy_wait_all();
+}
+
+template <int D, int NT>
+__device__ __forceinline__ void consume(Shared<D, NT> &sm, const AttnArgs &a, int warp)
+{
+    using S = Shared<D, NT>;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int tile = warp % kProducers;
+    const int mrow = (lane & 7) + ((lane >> 3) & 1) * 8, mgrp = lane >> 4;   // ldmatrix: this lane's row
     uint32_t qf[NT][D / 16][2];       // queries as the second operand
-    float qc[NT][2];                  // scale * log2 e * the power of two taken out, of heads 2t, 2t + 1
+    float qc[NT][2];                  // factors of heads 2t, 2t + 1
     float o[NT][D / 16][4];           // [dimension 16 j + 2 g, + 1][head 2t, 2t + 1]
     float m[NT][2], l[NT][2];
-    int item = -1;
-
-    for (int i = 0;; ++i) {
-        copy_wait<S::kAhead - 1>();
-        __syncwarp();
-        const Desc d = sm.desc[warp][i % kDescs];
-        if (d.flags & kEnd)
+    int slot = warp / kProducers;     // stages of this warp's half of the steps
+    uint32_t parity = 0;
+    int item = 0;
+    wait_for(sm, &sm.helped[0], 0);
+    while (true) {
+        wait_for(sm, &sm.full[slot], parity);
+        const Stage st = sm.stage[slot];
+        if ((st.flags & kEnd) || *static_cast<volatile int *>(&sm.dead))
             break;
-        ask_codes(i + S::kAhead);
-        {
-            const int flags = sm.desc[warp][(i + S::kAhead + 1) % kDescs].flags;
-            if ((flags & kFirst) && !(flags & kEnd))
-                ask_queries(i + S::kAhead + 1, asked_items++);
-        }
-        ask_pages(i + kIds);
-        copy_commit();
-        const int stage = i % S::kStages;
-
-        if (d.flags & kFirst) {
-            ++item;
+        if (st.flags & kFirst) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const uint2 *row = reinterpret_cast<const uint2 *>(&sm.q[item % kQueries][n * 8 + g][0]);
-                uint2 raw[D / 16];
-                uint32_t top = 0;     // the head's largest magnitude, bf16 bits
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    raw[ks] = row[ks * 4 + t];
-                    top = max(top, max(max(raw[ks].x & 0x7fffu, (raw[ks].x >> 16) & 0x7fffu),
-                                       max(raw[ks].y & 0x7fffu, (raw[ks].y >> 16) & 0x7fffu)));
+                for (int kp = 0; kp < D / 32; ++kp) {
+                    const uint4 x = sm.q[item & 1][n][kp][lane];
+                    qf[n][2 * kp][0] = x.x;
+                    qf[n][2 * kp][1] = x.y;
+                    qf[n][2 * kp + 1][0] = x.z;
+                    qf[n][2 * kp + 1][1] = x.w;
                 }
-                top = max(top, __shfl_xor_sync(kFull, top, 1));
-                top = max(top, __shfl_xor_sync(kFull, top, 2));
-                // largest magnitude to [2^14, 2^15)
-                const int e = top == 0 ? 0 : max(-120, static_cast<int>(top >> 7) - 127 - 14);
-                const float down = pow2(-e);
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    qf[n][ks][0] = pack_half(__uint_as_float(raw[ks].x << 16) * down, __uint_as_float(raw[ks].x & 0xffff0000u) * down);
-                    qf[n][ks][1] = pack_half(__uint_as_float(raw[ks].y << 16) * down, __uint_as_float(raw[ks].y & 0xffff0000u) * down);
-                }
-                const float c = a.scale * kLog2e * pow2(e);
-                // heads 2t and 2t + 1 are rows of lanes 8t and 8t + 4
-                qc[n][0] = __shfl_sync(kFull, c, 8 * t);
-                qc[n][1] = __shfl_sync(kFull, c, 8 * t + 4);
+                qc[n][0] = sm.qc[item & 1][n * 8 + 2 * t];
+                qc[n][1] = sm.qc[item & 1][n * 8 + 2 * t + 1];
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j)
 #pragma unroll
@@ -542,12 +467,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
                 l[n][0] = l[n][1] = 0.0f;
             }
         }
-
-        if (d.flags & (kHalf0 | kHalf1)) {
-            const float4 sc = sm.scale[warp][stage];
-            const uint32_t ks_base = smem_u32(&sm.ring[warp][stage][0][0]);
+        const int key0 = st.key0 + tile * kTile;
+        if (key0 < st.hi && key0 + kTile > st.lo) {
+            const uint32_t ks_base = smem_u32(&sm.ring[slot][tile][0][0]);
             const uint32_t vs_base = ks_base + S::kMatrix;
-            const int mrow = (lane & 7) + ((lane >> 3) & 1) * 8, mgrp = lane >> 4;   // ldmatrix: this lane's row
             // scores of 32 positions: rows g and g + 8 of two tiles of 16
             float s[NT][2][4];
 #pragma unroll
@@ -573,12 +496,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
                     }
                 }
             // base-2 exponents t_j, and their maximum
+            const float4 sc = sm.scale[slot][tile];
             const float sk[2] = {checked_scale(sc.x), checked_scale(sc.y)};
             const float sv[2] = {checked_scale(sc.z), checked_scale(sc.w)};
             // approximate to 2^-22: a page's weights are all off by the same factor, less than 2^-21
             const float lsv[2] = {log2_approx(sv[0]), log2_approx(sv[1])};
             const float rsv[2] = {rcp_approx(sv[0]), rcp_approx(sv[1])};
-            const bool whole = (d.flags & kWhole) != 0;
+            const bool whole = key0 >= st.lo && key0 + kTile <= st.hi;
             uint32_t pf[NT][2][2];    // weights as the second operand: [tile of 16][keys 0-7, 8-15]
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -595,8 +519,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
                     for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
-                            const int key = d.key0 + mt * 16 + g + (x >> 1) * 8;
-                            if (key < d.lo || key >= d.hi)
+                            const int key = key0 + mt * 16 + g + (x >> 1) * 8;
+                            if (key < st.lo || key >= st.hi)
                                 s[n][mt][x] = -INFINITY;
                         }
                 }
@@ -629,8 +553,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
                     l[n][h] = fmaf(l[n][h], corr[h], sum[h]);
                     m[n][h] = mx[h];
                 }
-                // outputs so far to the new maximum (factors of one change nothing)
-                if (!(d.flags & kFirst)) {
+                // outputs so far to the new maximum
+                if (!(st.flags & kFirst)) {
 #pragma unroll
                     for (int j = 0; j < D / 16; ++j) {
                         o[n][j][0] *= corr[0];
@@ -659,13 +583,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
                     }
                 }
         }
-
-        if (d.flags & kLast) {
-            // this warp's state to its (consumed) stage, then the eight states added in warp order
-            float *mine = reinterpret_cast<float *>(&sm.ring[warp][stage][0][0]);
-            __syncwarp();   // every lane has read the stage's codes
+        warp_arrive(&sm.empty[slot]);
+        slot += 2;
+        if (slot >= S::kStages) {
+            slot -= S::kStages;
+            parity ^= 1;
+        }
+        if (st.flags & kLast) {
+            ++item;
+            wait_for(sm, &sm.helped[item & 1], (item >> 1) & 1);   // the states of the item before have been read
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float x = l[n][h];
@@ -678,48 +606,185 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
                     if (head < a.group) {
 #pragma unroll
                         for (int j = 0; j < D / 16; ++j)
-                            *reinterpret_cast<float2 *>(mine + out_offset<D>(head, 16 * j + 2 * g)) =
+                            *reinterpret_cast<float2 *>(&sm.state[warp][0][0] + state_offset<D>(head, 16 * j + 2 * g)) =
                                 make_float2(o[n][j][h], o[n][j][2 + h]);
                     }
                 }
-            }
-            __syncthreads();
-            constexpr int kPairs = D / 2;
-            for (int x = tid; x < a.group * kPairs; x += kThreads) {
-                const int head = x / kPairs, dd = (x % kPairs) * 2;
-                float mx = -INFINITY;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w)
-                    mx = fmaxf(mx, sm.ml[w][head].x);
-                float sum = 0.0f;
-                float2 acc = make_float2(0.0f, 0.0f);
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float2 ml = sm.ml[w][head];
-                    const float2 v = *reinterpret_cast<const float2 *>(
-                        reinterpret_cast<const float *>(&sm.ring[w][stage][0][0]) + out_offset<D>(head, dd));
-                    const float f = exp2_approx(ml.x - mx);
-                    sum = fmaf(ml.y, f, sum);
-                    acc.x = fmaf(v.x, f, acc.x);
-                    acc.y = fmaf(v.y, f, acc.y);
-                }
-                const int64_t row = static_cast<int64_t>(d.b) * a.hq + d.kvh * a.group + head;
-                if (d.chunks == 1) {
-                    const bool bad = (d.flags & kBad) != 0, empty = d.hi <= d.lo;
-                    const float r0 = bad ? NAN : empty ? 0.0f : acc.x / sum, r1 = bad ? NAN : empty ? 0.0f : acc.y / sum;
-                    *reinterpret_cast<__nv_bfloat162 *>(a.out + d.b * a.ldo + static_cast<int64_t>(d.kvh * a.group + head) * D + dd) =
-                        __floats2bfloat162_rn(r0, r1);
-                    if (a.lse && dd == 0)
-                        a.lse[row] = bad ? NAN : empty ? -INFINITY : (mx - kWeightExp + log2f(sum)) * kLn2;
-                } else {
-                    const int64_t at = row * a.chunks + d.chunk;
-                    *reinterpret_cast<float2 *>(a.part + at * D + dd) = acc;
-                    if (dd == 0)
-                        a.part_ml[at] = make_float2(mx, sum);
-                }
-            }
-            __syncthreads();   // the stages are refilled from the next tile on
+            warp_arrive(&sm.states);
         }
+    }
+}
+
+// Queries of an item, as the consumers' lanes hold them: helper warp w converts heads w, w + 4, ...
+template <int D, int NT>
+__device__ __forceinline__ void prepare_queries(Shared<D, NT> &sm, const AttnArgs &a, const Items &it, int buf, int w)
+{
+    const int lane = threadIdx.x & 31;
+    for (int head = w; head < a.group; head += kHelpers) {
+        uint2 raw = make_uint2(0, 0);
+        if (lane < D / 4)   // four dimensions a lane
+            raw = *(reinterpret_cast<const uint2 *>(a.q + it.b * a.ldq + static_cast<int64_t>(it.kvh * a.group + head) * D) + lane);
+        uint32_t top = max(max(raw.x & 0x7fffu, (raw.x >> 16) & 0x7fffu), max(raw.y & 0x7fffu, (raw.y >> 16) & 0x7fffu));
+        top = __reduce_max_sync(kFull, top);
+        // the largest magnitude goes to [2^14, 2^15)
+        const int e = top == 0 ? 0 : max(-120, static_cast<int>(top >> 7) - 127 - 14);
+        const float down = pow2(-e);
+        if (lane < D / 4) {
+            uint2 x;
+            x.x = pack_half(__uint_as_float(raw.x << 16) * down, __uint_as_float(raw.x & 0xffff0000u) * down);
+            x.y = pack_half(__uint_as_float(raw.y << 16) * down, __uint_as_float(raw.y & 0xffff0000u) * down);
+            const int ks = lane >> 2;
+            reinterpret_cast<uint2 *>(&sm.q[buf][head >> 3][ks >> 1][(head & 7) * 4 + (lane & 3)])[ks & 1] = x;
+        }
+        if (lane == 0)
+            sm.qc[buf][head] = a.scale * kLog2e * pow2(e);
+    }
+}
+
+// The eight states of an item added in warp order, and the result or the chunk's part stored.
+template <int D, int NT>
+__device__ __forceinline__ void add_states(Shared<D, NT> &sm, const AttnArgs &a, const Items &it, int tid)
+{
+    constexpr int kQuads = D / 4;
+    for (int x = tid; x < a.group * kQuads; x += 32 * kHelpers) {
+        const int head = x / kQuads, dd = (x % kQuads) * 4;
+        float2 ml[kConsumers];
+        float mx = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kConsumers; ++w) {
+            ml[w] = sm.ml[w][head];
+            mx = fmaxf(mx, ml[w].x);
+        }
+        float sum = 0.0f;
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < kConsumers; ++w) {
+            const float4 v = *reinterpret_cast<const float4 *>(&sm.state[w][0][0] + state_offset<D>(head, dd));
+            const float f = exp2_approx(ml[w].x - mx);
+            sum = fmaf(ml[w].y, f, sum);
+            acc.x = fmaf(v.x, f, acc.x);
+            acc.y = fmaf(v.y, f, acc.y);
+            acc.z = fmaf(v.z, f, acc.z);
+            acc.w = fmaf(v.w, f, acc.w);
+        }
+        const int h = it.kvh * a.group + head;
+        const int64_t row = static_cast<int64_t>(it.b) * a.hq + h;
+        const bool bad = it.bad || *static_cast<volatile int *>(&sm.dead), empty = it.hi <= it.lo;
+        if (it.chunks == 1) {
+            const float r = bad ? NAN : empty ? 0.0f : 1.0f / sum;
+            if (empty || bad)
+                acc = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+            uint2 y;
+            *reinterpret_cast<__nv_bfloat162 *>(&y.x) = __floats2bfloat162_rn(acc.x * r, acc.y * r);
+            *reinterpret_cast<__nv_bfloat162 *>(&y.y) = __floats2bfloat162_rn(acc.z * r, acc.w * r);
+            *reinterpret_cast<uint2 *>(a.out + it.b * a.ldo + static_cast<int64_t>(h) * D + dd) = y;
+            if (a.lse && dd == 0)
+                a.lse[row] = bad ? NAN : empty ? -INFINITY : (mx - kWeightExp + log2f(sum)) * kLn2;
+        } else {
+            const int64_t at = row * a.chunks + it.chunk;
+            *reinterpret_cast<float4 *>(a.part + at * D + dd) = acc;
+            if (dd == 0)
+                a.part_ml[at] = make_float2(mx, bad ? NAN : sum);
+        }
+    }
+}
+
+template <int D, int NT>
+__device__ __forceinline__ void help(Shared<D, NT> &sm, const AttnArgs &a, Items it, int w)
+{
+    Items now = it;                // the item whose states come next
+    for (int i = 0; i < 2 && !it.done(); ++i) {
+        prepare_queries(sm, a, it, i, w);
+        next_item(it, a, sm.first_chunk, sm.len);
+    }
+    warp_arrive(&sm.helped[0]);
+    warp_arrive(&sm.helped[1]);
+    for (int item = 0; !now.done(); ++item) {
+        wait_for(sm, &sm.states, item & 1);
+        add_states(sm, a, now, threadIdx.x - 32 * kConsumers);
+        next_item(now, a, sm.first_chunk, sm.len);
+        if (!it.done()) {
+            prepare_queries(sm, a, it, item & 1, w);
+            next_item(it, a, sm.first_chunk, sm.len);
+        }
+        if (!now.done())
+            warp_arrive(&sm.helped[item & 1]);
+    }
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __grid_constant__ AttnArgs a)
+{
+    using S = Shared<D, NT>;
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    S &sm = *reinterpret_cast<S *>(smem_raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid < S::kStages) {
+        bi::ptx::mbar_init(&sm.full[tid], 33 * kProducers);   // every copying thread, and one plain arrival a warp
+        bi::ptx::mbar_init(&sm.empty[tid], kConsumers / 2);
+    }
+    if (tid == 0) {
+        bi::ptx::mbar_init(&sm.states, kConsumers);
+        bi::ptx::mbar_init(&sm.helped[0], kHelpers);
+        bi::ptx::mbar_init(&sm.helped[1], kHelpers);
+        bi::ptx::fence_mbarrier_init();
+        sm.dead = 0;
+    }
+    // query columns that no head fills stay zero
+    for (int x = tid; x < 2 * NT * (D / 32) * 32; x += kThreads)
+        (&sm.q[0][0][0][0])[x] = make_uint4(0, 0, 0, 0);
+    if (tid < 2 * S::kCols)
+        (&sm.qc[0][0])[tid] = 0.0f;
+    bi_kv::dependency_wait();
+
+    // chunks before each entry, one thread an entry
+    const int per = (a.b + kEntries - 1) / kEntries;
+    static_assert(kThreads == kEntries, "one thread an entry");
+    int n = 0;
+    for (int b = tid * per; b < (tid + 1) * per && b < a.b; ++b) {
+        const int len = a.lens[b];
+        if (per == 1)
+            sm.len[tid] = len;
+        n += span_of(len, a).chunks;
+    }
+    int incl = n;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(kFull, incl, off);
+        if (lane >= off)
+            incl += y;
+    }
+    if (lane == 31)
+        sm.warp_sum[warp] = incl;
+    __syncthreads();
+    int before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        before += w < warp ? sm.warp_sum[w] : 0;
+        total += sm.warp_sum[w];
+    }
+    // the entry behind the last sequence ends the scan, the others behind it hold INT_MAX
+    sm.first_chunk[tid] = tid <= (a.b + per - 1) / per ? before + incl - n : INT_MAX;
+    __syncthreads();
+
+    Items it;
+    it.item = blockIdx.x;
+    it.items = total * a.heads;
+    it.stride = gridDim.x;
+    it.u = it.item / a.heads;
+    it.kvh = it.item - it.u * a.heads;
+    it.du = it.stride / a.heads;
+    it.dh = it.stride - it.du * a.heads;
+    if (it.done())
+        return;
+    if (warp < kConsumers) {
+        consume(sm, a, warp);
+    } else {
+        open_item(it, a, sm.first_chunk, sm.len);
+        if (warp < kConsumers + kHelpers)
+            help(sm, a, it, warp - kConsumers);
+        else
+            produce(sm, a, it, warp - kConsumers - kHelpers);
     }
     bi_kv::launch_dependents();
 }

@@ -2,6 +2,7 @@
 // handle, the device probe, launches as programmatic dependents, and the limits of a scale.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -35,7 +36,7 @@ inline bi_status_t check_cache(const bi_kv_cache_t *c)
     if (!valid_page_size(c->page_size) || (c->head_dim != 64 && c->head_dim != 128) ||
         c->num_pages > INT32_MAX / c->page_size || c->num_heads > 65535)
         return BI_ERR_UNSUPPORTED_SHAPE;
-    const int64_t d = c->head_dim, big = INT64_C(1) << 40;
+    const int64_t d = c->head_dim, big = (INT64_C(1) << 40) - 16;
     if (c->token_stride < d || c->head_stride < d)
         return BI_ERR_INVALID_ARG;
     if (c->token_stride > big || c->head_stride > big || c->page_stride > big)
@@ -86,6 +87,35 @@ inline bi_status_t current_device(int *dev_out, int *num_sms)
     *dev_out = dev;
     *num_sms = d.sms;
     return BI_OK;
+}
+
+// The tensor map of one pool, [page][head][position][dimension], whose boxes are 16 positions (pages
+// of 16) or 32 of one page and head, in the swizzle that spreads rows of 64 or 128 bytes over the banks.
+inline bi_status_t page_map(CUtensorMap *map, const bi_kv_cache_t *c, void *pool)
+{
+    typedef CUresult (*Encode)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                               const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void *fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const bool ok = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) == cudaSuccess &&
+                        q == cudaDriverEntryPointSuccess;
+        return ok ? reinterpret_cast<Encode>(fn) : nullptr;
+    }();
+    if (!encode)
+        return BI_ERR_CUDA;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c->head_dim), static_cast<cuuint64_t>(c->page_size),
+                                static_cast<cuuint64_t>(c->num_heads), static_cast<cuuint64_t>(c->num_pages)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(c->token_stride), static_cast<cuuint64_t>(c->head_stride),
+                                   static_cast<cuuint64_t>(c->page_stride)};
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>(c->head_dim), c->page_size == 16 ? 16u : 32u, 1, 1};
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, pool, dims, strides, box, ones,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              c->head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? BI_OK : BI_ERR_CUDA;
 }
 
 // Launch as a programmatic dependent of the previous kernel in the stream: the grid may start

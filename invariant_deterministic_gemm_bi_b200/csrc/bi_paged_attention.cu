@@ -11,12 +11,12 @@
 // states are added in warp order at the chunk's end, and the chunks in ascending order by a second
 // kernel.  Every sum's order is thus fixed by the sequence's length and window.
 //
-// Roles (16 warps, one CTA per SM).  Four producer warps stream half-steps of 128 positions into a
-// ring of stages, one tile of 32 positions each, with cp.async: rows outside the sequence are
-// filled with zeros, so a stale NaN code cannot reach a sum through a zero weight.  Eight consumer
-// warps do nothing but the matrix products and the softmax.  Four helper warps prepare the next
-// items' queries and add the states of the chunks that are done.  (With the three jobs in every
-// warp, a tile took 964 warp instructions, 149 us for 64 sequences of 4096 positions, 32/8 heads.)
+// Roles (12 warps, one CTA per SM).  One producer warp streams half-steps of 128 positions into a
+// ring of stages with TMA (boxes of 16 or 32 positions of one page and head).  Eight consumer warps
+// do nothing but the matrix products and the softmax.  Three helper warps prepare the next items'
+// queries, add the states of the chunks that are done and keep the table of items filled.  (With
+// all jobs in every warp, a tile took 964 warp instructions, 149 us for 64 sequences of 4096
+// positions, 32/8 heads; with four producer warps and cp.async 865, 108 us.)
 //
 // Matrix products.  The cache is the first operand of mma.m16n8k16 (16 positions, or 16 dimensions,
 // a time) and the query heads are the 8 columns, so grouped queries fill the tile instead of
@@ -33,6 +33,7 @@
 // rounded to fp16 (2^-11 of itself, a quarter of what bf16 would cost; the output is rounded to bf16
 // anyway); the softmax sum adds a_j / sv in fp32.  The value scale so costs nothing per element and
 // weights down to 2^-29 of the largest keep all of fp16's bits, whatever the scales.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -51,15 +52,18 @@ namespace {
 using bi_kv::kFull;
 
 constexpr int kConsumers = 8;               // warps, as for the next two
-constexpr int kHelpers = 4;
-constexpr int kProducers = 4;
+constexpr int kHelpers = 3;
+constexpr int kProducers = 1;
 constexpr int kThreads = 32 * (kConsumers + kHelpers + kProducers);
 constexpr int kTile = 32;                   // positions of a warp's tile
-constexpr int kHalf = kProducers * kTile;   // positions of a stage: half a step
+constexpr int kTiles = 4;                   // tiles of a stage
+constexpr int kHalf = kTiles * kTile;       // positions of a stage: half a step
 constexpr int kStep = kConsumers * kTile;   // positions of a CTA's step
 constexpr int kMaxChunks = 128;             // chunks of a sequence
 constexpr int kMaxGroup = 16;               // query heads of a key/value head
 constexpr int kEntries = 512;               // entries of the scanned chunk counts
+constexpr int kItemBlock = 32;              // items whose table entries one warp makes at once
+constexpr int kItemRing = 4 * kItemBlock;   // entries of the items' table
 constexpr int kMaxBatch = kEntries * 32;    // an entry stands for up to 32 sequences
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -82,15 +86,13 @@ __host__ __device__ __forceinline__ int chunk_steps(int steps)
 
 struct AttnArgs {
     const __nv_bfloat16 *q;
-    const uint8_t *k, *v;
     const float *k_scale, *v_scale;
     const int32_t *table, *lens;
     __nv_bfloat16 *out;
     float *lse;
     float *part;        // [b][hq][chunks][D] unnormalised outputs
     float2 *part_ml;    // [b][hq][chunks] (M, sum)
-    int64_t ldq, ldo, ld_table, page_stride, token_stride, head_stride;
-    int64_t window;
+    int64_t ldq, ldo, ld_table, window;
     int num_pages, max_len, b, hq, heads, group, page_shift, chunks;
     float scale;
 };
@@ -121,17 +123,17 @@ __device__ __forceinline__ Span span_of(int len, const AttnArgs &a)
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
-// 16 bytes, or 16 zero bytes when `valid` is false (nothing is read then)
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool valid)
+// one box of codes: positions [pos, pos + rows) of a page's head, all dimensions
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int pos, int head, int page)
 {
-    const int n = valid ? 16 : 0;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
+                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(pos), "r"(head), "r"(page)
+                 : "memory");
 }
-__device__ __forceinline__ void copy4(uint32_t dst, const void *src)
+__device__ __forceinline__ void expect_bytes(uint64_t *bar, uint32_t bytes)
 {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr)
 {
@@ -202,16 +204,31 @@ struct Stage {
     int key0, lo, hi, flags;
 };
 
-template <int D, int NT>
+// One chunk of one key/value head.
+struct Item {
+    int b, kvh;          // b < 0: no more items
+    int lo, hi;          // the sequence's attended positions
+    int key0, steps;     // the chunk's first position and length
+    int chunk, chunks;   // chunk < 0: the sequence's length is out of range
+};
+static_assert(sizeof(Item) == 32, "two 16-byte words");
+
+// MG: the most query heads of a key/value head, 4, 8 or 16 (columns come in eights).
+template <int D, int MG>
 struct Shared {
+    static constexpr int NT = MG > 8 ? 2 : 1;
     static constexpr int kCols = NT * 8;
-    // 32 KB stages of D = 128 (16 KB of D = 64) beside the chunk states, 192 KB together at most
-    static constexpr int kStages = D == 128 ? (NT == 1 ? 5 : 4) : 8;
+    // 32 KB stages of D = 128 (16 KB of D = 64) beside the chunk states, 208 KB together at most.  A
+    // stage always serves the same half of the steps: a consumer then waits for every use of its
+    // stages in turn, which waiting by parity needs.
+    static constexpr int kStages = D == 128 ? (MG == 4 ? 6 : 4) : 10;
+    static_assert(kStages % 2 == 0, "two halves");
     static constexpr int kMatrix = kTile * D;               // bytes of a tile's keys (or values)
-    uint8_t ring[kStages][kProducers][2][kMatrix];
-    float state[kConsumers][kCols][D];                      // a chunk's outputs, not normalised
+    uint8_t ring[kStages][kTiles][2][kMatrix];              // keys, values
+    float state[kConsumers][MG][D];                         // a chunk's outputs, not normalised
     uint4 q[2][NT][D / 32][32];                             // two items' queries, as the consumers' lanes hold them
-    float4 scale[kStages][kProducers];                      // of a tile's two 16s: key scales, value scales
+    float4 scale[kStages][kHalf / 16];                      // of 16 positions: key scale, log2 and 1 / of the value scale
+    Item items[kItemRing];
     Stage stage[kStages];
     float2 ml[kConsumers][kCols];                           // a chunk's maxima and sums
     float qc[2][kCols];                                     // scale * log2 e * the power of two taken out
@@ -219,7 +236,7 @@ struct Shared {
     // A chunk's states are written; the helpers have read the states of the item before and prepared
     // the queries of the one after (even and odd items apart: the helpers may be one ahead).
     uint64_t states, helped[2];
-    int32_t first_chunk[kEntries + 32];                     // chunks before each entry
+    int32_t first_chunk[kEntries];                          // chunks before each entry
     int32_t len[kEntries];                                  // lengths, when an entry is one sequence
     int32_t warp_sum[kThreads / 32];
     int dead;                                               // a wait gave up
@@ -256,187 +273,162 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar)
         bi::ptx::mbar_arrive(bar);
 }
 
-// One arrival on `bar` once every cp.async of this thread so far has landed.
-__device__ __forceinline__ void arrive_after_copies(uint64_t *bar)
+// Item number i of this CTA: chunk ordinal u of the scan and a key/value head, one lane an item.
+__device__ __forceinline__ Item make_item(const AttnArgs &a, const int32_t *first_chunk, const int32_t *len_s, int total, int i)
 {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
-// Walks the items of this CTA, one chunk of one key/value head each.
-struct Items {
-    int item, items, stride;   // item = chunk ordinal * heads + key/value head
-    int u, du, dh;             // chunk ordinal; the stride's quotient and remainder by the heads
-    int b, kvh, lo, hi, chunk, chunks, steps, key0;
-    bool bad;
-
-    __device__ __forceinline__ bool done() const { return item >= items; }
-};
-
-// The sequence and chunk of chunk ordinal it.u (all lanes alike).
-__device__ __forceinline__ void open_item(Items &it, const AttnArgs &a, const int32_t *first_chunk, const int32_t *len_s)
-{
-    const int lane = threadIdx.x & 31;
-    // the last entry with first_chunk <= u: 16 entries a lane, then one
-    const int blk = __popc(__ballot_sync(kFull, first_chunk[lane * 16] <= it.u)) - 1;
-    const int e = blk * 16 + __popc(__ballot_sync(kFull, lane < 16 && first_chunk[blk * 16 + (lane & 15)] <= it.u)) - 1;
-    int chunk = it.u - first_chunk[e], b = e;
+    Item it = {};
+    const int64_t n = blockIdx.x + static_cast<int64_t>(i) * gridDim.x;
+    it.b = -1;
+    if (n >= static_cast<int64_t>(total) * a.heads)
+        return it;
+    const int u = static_cast<int>(n / a.heads);
+    it.kvh = static_cast<int>(n - static_cast<int64_t>(u) * a.heads);
+    int e = 0;   // the last entry with first_chunk <= u
+#pragma unroll
+    for (int step = kEntries / 2; step > 0; step >>= 1)
+        if (first_chunk[e + step] <= u)
+            e += step;
+    int chunk = u - first_chunk[e], b = e;
     Span s;
     if (a.b <= kEntries) {
         s = span_of(len_s[b], a);
-    } else {
-        // an entry is `per` consecutive sequences
-        const int per = (a.b + kEntries - 1) / kEntries;
-        const int mine = e * per + lane;
-        const bool own = lane < per && mine < a.b;
-        const Span x = span_of(own ? a.lens[mine] : 0, a);
-        const int n = own ? x.chunks : 0;
-        int incl = n;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int y = __shfl_up_sync(kFull, incl, off);
-            if (lane >= off)
-                incl += y;
-        }
-        const int at = __ffs(__ballot_sync(kFull, incl > chunk)) - 1;
-        chunk -= __shfl_sync(kFull, incl - n, at);
-        b = e * per + at;
+    } else {   // an entry is several consecutive sequences
+        b = e * ((a.b + kEntries - 1) / kEntries);
         s = span_of(a.lens[b], a);
+        while (chunk >= s.chunks) {
+            chunk -= s.chunks;
+            s = span_of(a.lens[++b], a);
+        }
     }
     it.b = b;
     it.lo = s.lo;
     it.hi = s.hi;
-    it.bad = s.bad;
-    it.chunk = chunk;
-    it.chunks = s.chunks;
-    it.steps = min(s.per_chunk, s.steps - chunk * s.per_chunk);
     it.key0 = (s.first + chunk * s.per_chunk) * kStep;
-}
-
-__device__ __forceinline__ void next_item(Items &it, const AttnArgs &a, const int32_t *first_chunk, const int32_t *len_s)
-{
-    it.item += it.stride;
-    it.u += it.du;
-    it.kvh += it.dh;
-    if (it.kvh >= a.heads) {
-        it.kvh -= a.heads;
-        ++it.u;
-    }
-    if (!it.done())
-        open_item(it, a, first_chunk, len_s);
+    it.steps = min(s.per_chunk, s.steps - chunk * s.per_chunk);
+    it.chunk = s.bad ? -1 : chunk;
+    it.chunks = s.chunks;
+    return it;
 }
 
 // ---------------------------------------------------------------------------------------------
 // the roles
 // ---------------------------------------------------------------------------------------------
 
-// Producer warp p copies tile p of every stage.
-template <int D, int NT>
-__device__ __forceinline__ void produce(Shared<D, NT> &sm, const AttnArgs &a, Items it, int p)
+// The producer warp.  Lane 8 s + j stands for the j-th 16 positions of stage s of a block of four
+// stages; it holds their page number, asked for one block ahead, and scales, asked for half a block
+// ahead.
+template <int D, int MG>
+__device__ __forceinline__ void produce(Shared<D, MG> &sm, const AttnArgs &a, const CUtensorMap *k_map, const CUtensorMap *v_map)
 {
-    using S = Shared<D, NT>;
-    constexpr int kGroups = D / 16;        // 16-byte groups of a row
-    constexpr int kRows = 32 / kGroups;    // rows one copy instruction covers
-    const int lane = threadIdx.x & 31;
+    using S = Shared<D, MG>;
+    constexpr int kBlock = 4;              // stages
+    const int lane = threadIdx.x & 31, group = lane & 7, quarter = lane >> 3;
+    const int box = a.page_shift == 4 ? 16 : kTile;   // positions of a TMA box
     const int page_mask = (1 << a.page_shift) - 1;
-    // this lane's 16-byte group and first row, in the cache and in shared memory
-    const int grp = lane % kGroups, row0 = lane / kGroups;
-    const int64_t lane_at = row0 * a.token_stride + grp * 16, row_step = kRows * a.token_stride;
-    const uint32_t lane_dst = tile_offset<D>(row0, grp);
 
-    // lanes 0 and 1 hold the page numbers of the tile's first and second 16 positions
-    auto page_of = [&](const Items &x, int key0) {
-        const int key = key0 + p * kTile + lane * (kTile / 2);
-        return !x.done() && lane < 2 && key < x.hi && key + kTile / 2 > x.lo
-                   ? a.table[x.b * a.ld_table + (key >> a.page_shift)]
-                   : -1;
+    // this lane's box of a block: whether any of it is attended, and its page
+    struct Pages {
+        int key, id;
+        bool in, ok;
     };
+    auto pages_of = [&](const Item &it, int block) {
+        Pages x;
+        x.key = it.key0 + (block * kBlock + quarter) * kHalf + (group * 16 & ~(box - 1));
+        x.in = it.b >= 0 && block * kBlock + quarter < 2 * it.steps && x.key < it.hi && x.key + box > it.lo;
+        x.id = x.in ? a.table[it.b * a.ld_table + (x.key >> a.page_shift)] : -1;
+        x.ok = false;
+        return x;
+    };
+    struct Scales {
+        float k, v;
+    };
+    auto scales_of = [&](const Item &it, Pages &x) {
+        x.ok = x.in && x.id >= 0 && x.id < a.num_pages;
+        const int64_t at = static_cast<int64_t>(x.id) * a.heads + it.kvh;
+        Scales s = {x.in ? NAN : 1.0f, 1.0f};   // a page number out of range gives NaN
+        if (x.ok)
+            s = {a.k_scale[at], a.v_scale[at]};
+        return s;
+    };
+
     int slot = 0;
     uint32_t parity = 1;     // of a stage not used yet
-    int half = 0;            // of the current item
-    int mine = page_of(it, it.key0);
-    while (true) {
-        const bool end = it.done();
-        const int key0 = it.key0 + half * kHalf;
-        const int kvh = it.kvh;
-        const Stage st = {key0, it.lo, it.hi,
-                          end ? kEnd : (half < 2 ? kFirst : 0) | (half >= 2 * it.steps - 2 ? kLast : 0)};
-        const int id[2] = {__shfl_sync(kFull, mine, 0), __shfl_sync(kFull, mine, 1)};
-        // the next stage's page numbers come while this one waits for its place
-        if (++half == (end ? 2 : 2 * it.steps) && !end) {
-            half = 0;
-            next_item(it, a, sm.first_chunk, sm.len);
-        }
-        mine = page_of(it, it.key0 + half * kHalf);
-
-        wait_for(sm, &sm.empty[slot], parity);
-        if (p == 0 && lane == 0)
-            sm.stage[slot] = st;
-        const int tile0 = key0 + p * kTile;
-        if (!end && tile0 < st.hi && tile0 + kTile > st.lo) {
-            int64_t base[2];
-            bool ok[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int key = tile0 + h * (kTile / 2);
-                const bool in = key < st.hi && key + kTile / 2 > st.lo;
-                ok[h] = in && id[h] >= 0 && id[h] < a.num_pages;
-                base[h] = ok[h] ? id[h] * a.page_stride + (key & page_mask) * a.token_stride + kvh * a.head_stride : 0;
-                if (lane == h || lane == h + 2) {   // lanes 0, 1: key scales, 2, 3: value scales
-                    float *dst = reinterpret_cast<float *>(&sm.scale[slot][p]) + lane;
-                    if (ok[h])
-                        copy4(smem_u32(dst), (lane < 2 ? a.k_scale : a.v_scale) + static_cast<int64_t>(id[h]) * a.heads + kvh);
-                    else
-                        *dst = in ? NAN : 1.0f;     // a page number out of range
-                }
-            }
-            const uint32_t dst = smem_u32(&sm.ring[slot][p][0][0]);
-            if (ok[0] && ok[1] && tile0 >= st.lo && tile0 + kTile <= st.hi) {
-                // whole; the swizzle of rows kRows apart repeats after one or two of them
-                const int64_t from[2] = {base[0] + lane_at, base[1] + lane_at};
-#pragma unroll
-                for (int r = 0; r < kTile; r += kRows) {
-                    const int64_t at = from[r / (kTile / 2)] + (r % (kTile / 2)) / kRows * row_step;
-                    const uint32_t off = dst + r * D + (D == 128 && (r & 4) ? lane_dst ^ 64 : lane_dst);
-                    copy16(off, a.k + at, true);
-                    copy16(off + S::kMatrix, a.v + at, true);
-                }
-            } else {
-#pragma unroll
-                for (int r = 0; r < kTile; r += kRows) {
-                    const int row = r + row0, h = r / (kTile / 2);
-                    const int key = tile0 + row;
-                    const bool valid = ok[h] && key >= st.lo && key < st.hi;
-                    const int64_t at = valid ? base[h] + lane_at + (r % (kTile / 2)) / kRows * row_step : 0;
-                    const uint32_t off = dst + tile_offset<D>(row, grp);
-                    copy16(off, a.k + at, valid);
-                    copy16(off + S::kMatrix, a.v + at, valid);
-                }
-            }
-        }
-        arrive_after_copies(&sm.full[slot]);
-        warp_arrive(&sm.full[slot]);   // releases the words stored above
+    auto take_slot = [&]() { wait_for(sm, &sm.empty[slot], parity); };
+    auto give_slot = [&]() {
+        warp_arrive(&sm.full[slot]);   // releases the words stored for it
         if (++slot == S::kStages) {
             slot = 0;
             parity ^= 1;
         }
-        if ((end && half == 2) || *static_cast<volatile int *>(&sm.dead))
-            break;
+    };
+
+    int item = 0, block = 0;
+    Item it = sm.items[0];
+    Pages px = pages_of(it, 0);
+    Scales sc = scales_of(it, px);
+    while (it.b >= 0 && !*static_cast<volatile int *>(&sm.dead)) {
+        const int stages = min(kBlock, 2 * it.steps - block * kBlock);
+        // the next block, of this item or of the next one
+        int next_block = block + 1;
+        Item next = it;
+        if (next_block * kBlock >= 2 * it.steps) {
+            next_block = 0;
+            next = sm.items[++item % kItemRing];
+        }
+        Pages px_next = pages_of(next, next_block);
+        Scales sc_next = {1.0f, 1.0f};
+        for (int s = 0; s < stages; ++s) {
+            take_slot();
+            const bool mine = quarter == s;
+            const bool issue = mine && px.ok && (group * 16 & (box - 1)) == 0;
+            const uint32_t boxes = __popc(__ballot_sync(kFull, issue));
+            if (lane == 0) {
+                const int at = block * kBlock + s;
+                sm.stage[slot] = {it.key0 + at * kHalf, it.lo, it.hi,
+                                  (at < 2 ? kFirst : 0) | (at >= 2 * it.steps - 2 ? kLast : 0)};
+                expect_bytes(&sm.full[slot], boxes * 2u * box * D);
+            }
+            __syncwarp();
+            if (issue) {
+                const uint32_t dst = smem_u32(&sm.ring[slot][group >> 1][0][0]) + (group & 1) * 16 * D;
+                tma_box(dst, k_map, &sm.full[slot], px.key & page_mask, it.kvh, px.id);
+                tma_box(dst + S::kMatrix, v_map, &sm.full[slot], px.key & page_mask, it.kvh, px.id);
+            }
+            if (mine) {
+                // approximate to 2^-22: a page's weights are all off by one factor below 2^-21
+                const float v = checked_scale(sc.v);
+                sm.scale[slot][group] = make_float4(checked_scale(sc.k), log2_approx(v), rcp_approx(v), 0.0f);
+            }
+            if (s == min(1, stages - 1))
+                sc_next = scales_of(next, px_next);
+            give_slot();
+        }
+        it = next;
+        block = next_block;
+        px = px_next;
+        sc = sc_next;
     }
-    copy_wait_all();
+    for (int half = 0; half < 2; ++half) {   // both halves of the consumers are told
+        take_slot();
+        if (lane == 0)
+            sm.stage[slot] = {0, 0, 0, kEnd};
+        give_slot();
+    }
 }
 
-template <int D, int NT>
-__device__ __forceinline__ void consume(Shared<D, NT> &sm, const AttnArgs &a, int warp)
+template <int D, int MG>
+__device__ __forceinline__ void consume(Shared<D, MG> &sm, const AttnArgs &a, int warp)
 {
-    using S = Shared<D, NT>;
+    using S = Shared<D, MG>;
+    constexpr int NT = S::NT;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int tile = warp % kProducers;
+    const int tile = warp % kTiles;
     const int mrow = (lane & 7) + ((lane >> 3) & 1) * 8, mgrp = lane >> 4;   // ldmatrix: this lane's row
     uint32_t qf[NT][D / 16][2];       // queries as the second operand
     float qc[NT][2];                  // factors of heads 2t, 2t + 1
     float o[NT][D / 16][4];           // [dimension 16 j + 2 g, + 1][head 2t, 2t + 1]
     float m[NT][2], l[NT][2];
-    int slot = warp / kProducers;     // stages of this warp's half of the steps
+    int slot = warp / kTiles;         // stages of this warp's half of the steps
     uint32_t parity = 0;
     int item = 0;
     wait_for(sm, &sm.helped[0], 0);
@@ -471,6 +463,18 @@ __device__ __forceinline__ void consume(Shared<D, NT> &sm, const AttnArgs &a, in
         if (key0 < st.hi && key0 + kTile > st.lo) {
             const uint32_t ks_base = smem_u32(&sm.ring[slot][tile][0][0]);
             const uint32_t vs_base = ks_base + S::kMatrix;
+            const bool whole = key0 >= st.lo && key0 + kTile <= st.hi;
+            if (!whole) {
+                // rows outside the sequence may hold anything: a NaN value would pass through a zero weight
+                const int key = key0 + lane;
+                if (key < st.lo || key >= st.hi) {
+#pragma unroll
+                    for (int x = 0; x < D / 16; ++x)
+                        *reinterpret_cast<uint4 *>(&sm.ring[slot][tile][1][lane * D + x * 16]) = make_uint4(0, 0, 0, 0);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the stage's next load comes after
+                }
+                __syncwarp();
+            }
             // scores of 32 positions: rows g and g + 8 of two tiles of 16
             float s[NT][2][4];
 #pragma unroll
@@ -496,13 +500,8 @@ __device__ __forceinline__ void consume(Shared<D, NT> &sm, const AttnArgs &a, in
                     }
                 }
             // base-2 exponents t_j, and their maximum
-            const float4 sc = sm.scale[slot][tile];
-            const float sk[2] = {checked_scale(sc.x), checked_scale(sc.y)};
-            const float sv[2] = {checked_scale(sc.z), checked_scale(sc.w)};
-            // approximate to 2^-22: a page's weights are all off by the same factor, less than 2^-21
-            const float lsv[2] = {log2_approx(sv[0]), log2_approx(sv[1])};
-            const float rsv[2] = {rcp_approx(sv[0]), rcp_approx(sv[1])};
-            const bool whole = key0 >= st.lo && key0 + kTile <= st.hi;
+            const float4 sc[2] = {sm.scale[slot][2 * tile], sm.scale[slot][2 * tile + 1]};
+            const float sk[2] = {sc[0].x, sc[1].x}, lsv[2] = {sc[0].y, sc[1].y}, rsv[2] = {sc[0].z, sc[1].z};
             uint32_t pf[NT][2][2];    // weights as the second operand: [tile of 16][keys 0-7, 8-15]
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -616,8 +615,8 @@ __device__ __forceinline__ void consume(Shared<D, NT> &sm, const AttnArgs &a, in
 }
 
 // Queries of an item, as the consumers' lanes hold them: helper warp w converts heads w, w + 4, ...
-template <int D, int NT>
-__device__ __forceinline__ void prepare_queries(Shared<D, NT> &sm, const AttnArgs &a, const Items &it, int buf, int w)
+template <int D, int MG>
+__device__ __forceinline__ void prepare_queries(Shared<D, MG> &sm, const AttnArgs &a, const Item &it, int buf, int w)
 {
     const int lane = threadIdx.x & 31;
     for (int head = w; head < a.group; head += kHelpers) {
@@ -642,8 +641,8 @@ __device__ __forceinline__ void prepare_queries(Shared<D, NT> &sm, const AttnArg
 }
 
 // The eight states of an item added in warp order, and the result or the chunk's part stored.
-template <int D, int NT>
-__device__ __forceinline__ void add_states(Shared<D, NT> &sm, const AttnArgs &a, const Items &it, int tid)
+template <int D, int MG>
+__device__ __forceinline__ void add_states(Shared<D, MG> &sm, const AttnArgs &a, const Item &it, int tid)
 {
     constexpr int kQuads = D / 4;
     for (int x = tid; x < a.group * kQuads; x += 32 * kHelpers) {
@@ -669,7 +668,7 @@ __device__ __forceinline__ void add_states(Shared<D, NT> &sm, const AttnArgs &a,
         }
         const int h = it.kvh * a.group + head;
         const int64_t row = static_cast<int64_t>(it.b) * a.hq + h;
-        const bool bad = it.bad || *static_cast<volatile int *>(&sm.dead), empty = it.hi <= it.lo;
+        const bool bad = it.chunk < 0 || *static_cast<volatile int *>(&sm.dead), empty = it.hi <= it.lo;
         if (it.chunks == 1) {
             const float r = bad ? NAN : empty ? 0.0f : 1.0f / sum;
             if (empty || bad)
@@ -689,65 +688,79 @@ __device__ __forceinline__ void add_states(Shared<D, NT> &sm, const AttnArgs &a,
     }
 }
 
-template <int D, int NT>
-__device__ __forceinline__ void help(Shared<D, NT> &sm, const AttnArgs &a, Items it, int w)
+template <int D, int MG>
+__device__ __forceinline__ void help(Shared<D, MG> &sm, const AttnArgs &a, int total, int w)
 {
-    Items now = it;                // the item whose states come next
-    for (int i = 0; i < 2 && !it.done(); ++i) {
-        prepare_queries(sm, a, it, i, w);
-        next_item(it, a, sm.first_chunk, sm.len);
+    for (int i = 0; i < 2; ++i) {
+        const Item it = sm.items[i];
+        if (it.b >= 0)
+            prepare_queries(sm, a, it, i, w);
+        warp_arrive(&sm.helped[i]);
     }
-    warp_arrive(&sm.helped[0]);
-    warp_arrive(&sm.helped[1]);
-    for (int item = 0; !now.done(); ++item) {
-        wait_for(sm, &sm.states, item & 1);
+    for (int i = 0;; ++i) {
+        const Item now = sm.items[i % kItemRing];
+        if (now.b < 0)
+            break;
+        wait_for(sm, &sm.states, i & 1);
         add_states(sm, a, now, threadIdx.x - 32 * kConsumers);
-        next_item(now, a, sm.first_chunk, sm.len);
-        if (!it.done()) {
-            prepare_queries(sm, a, it, item & 1, w);
-            next_item(it, a, sm.first_chunk, sm.len);
+        const Item then = sm.items[(i + 2) % kItemRing];
+        if (then.b >= 0)
+            prepare_queries(sm, a, then, i & 1, w);
+        // The block of the table before item i's makes room for the one four further on: no helper
+        // warp is behind item i (its states were written after all of them had arrived for the item
+        // before), and the other warps read the new entries behind the barriers of the items between.
+        if (w == 0 && i > 0 && i % kItemBlock == 0) {
+            const int lane = threadIdx.x & 31, first = i - kItemBlock;
+            sm.items[(first + lane) % kItemRing] = make_item(a, sm.first_chunk, sm.len, total, first + kItemRing + lane);
         }
-        if (!now.done())
-            warp_arrive(&sm.helped[item & 1]);
+        warp_arrive(&sm.helped[i & 1]);
     }
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __grid_constant__ AttnArgs a)
+template <int D, int MG>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const __grid_constant__ AttnArgs a)
 {
-    using S = Shared<D, NT>;
-    extern __shared__ __align__(128) uint8_t smem_raw[];
+    using S = Shared<D, MG>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
     S &sm = *reinterpret_cast<S *>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid < S::kStages) {
-        bi::ptx::mbar_init(&sm.full[tid], 33 * kProducers);   // every copying thread, and one plain arrival a warp
-        bi::ptx::mbar_init(&sm.empty[tid], kConsumers / 2);
-    }
     if (tid == 0) {
+        for (int i = 0; i < S::kStages; ++i) {
+            bi::ptx::mbar_init(&sm.full[i], 1);
+            bi::ptx::mbar_init(&sm.empty[i], kTiles);
+        }
         bi::ptx::mbar_init(&sm.states, kConsumers);
         bi::ptx::mbar_init(&sm.helped[0], kHelpers);
         bi::ptx::mbar_init(&sm.helped[1], kHelpers);
         bi::ptx::fence_mbarrier_init();
+        bi::ptx::prefetch_tmap(&k_map);
+        bi::ptx::prefetch_tmap(&v_map);
         sm.dead = 0;
     }
     // query columns that no head fills stay zero
-    for (int x = tid; x < 2 * NT * (D / 32) * 32; x += kThreads)
+    for (int x = tid; x < 2 * S::NT * (D / 32) * 32; x += kThreads)
         (&sm.q[0][0][0][0])[x] = make_uint4(0, 0, 0, 0);
     if (tid < 2 * S::kCols)
         (&sm.qc[0][0])[tid] = 0.0f;
     bi_kv::dependency_wait();
 
-    // chunks before each entry, one thread an entry
+    // chunks before each entry: thread i scans entries 2 i and 2 i + 1
     const int per = (a.b + kEntries - 1) / kEntries;
-    static_assert(kThreads == kEntries, "one thread an entry");
-    int n = 0;
-    for (int b = tid * per; b < (tid + 1) * per && b < a.b; ++b) {
-        const int len = a.lens[b];
-        if (per == 1)
-            sm.len[tid] = len;
-        n += span_of(len, a).chunks;
+    static_assert(2 * kThreads >= kEntries, "two entries a thread");
+    int n[2] = {0, 0};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int e = 2 * tid + j;
+        if (e < kEntries)
+            for (int b = e * per; b < (e + 1) * per && b < a.b; ++b) {
+                const int len = a.lens[b];
+                if (per == 1)
+                    sm.len[e] = len;
+                n[j] += span_of(len, a).chunks;
+            }
     }
-    int incl = n;
+    int incl = n[0] + n[1];
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const int y = __shfl_up_sync(kFull, incl, off);
@@ -757,81 +770,120 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
     if (lane == 31)
         sm.warp_sum[warp] = incl;
     __syncthreads();
-    int before = 0, total = 0;
+    int before = incl - n[0] - n[1], total = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
         before += w < warp ? sm.warp_sum[w] : 0;
         total += sm.warp_sum[w];
     }
-    // the entry behind the last sequence ends the scan, the others behind it hold INT_MAX
-    sm.first_chunk[tid] = tid <= (a.b + per - 1) / per ? before + incl - n : INT_MAX;
-    __syncthreads();
-
-    Items it;
-    it.item = blockIdx.x;
-    it.items = total * a.heads;
-    it.stride = gridDim.x;
-    it.u = it.item / a.heads;
-    it.kvh = it.item - it.u * a.heads;
-    it.du = it.stride / a.heads;
-    it.dh = it.stride - it.du * a.heads;
-    if (it.done())
-        return;
-    if (warp < kConsumers) {
-        consume(sm, a, warp);
-    } else {
-        open_item(it, a, sm.first_chunk, sm.len);
-        if (warp < kConsumers + kHelpers)
-            help(sm, a, it, warp - kConsumers);
-        else
-            produce(sm, a, it, warp - kConsumers - kHelpers);
+    // entries behind the last sequence hold INT_MAX
+    const int used = (a.b + per - 1) / per;
+    if (2 * tid < kEntries) {
+        sm.first_chunk[2 * tid] = 2 * tid < used ? before : INT_MAX;
+        sm.first_chunk[2 * tid + 1] = 2 * tid + 1 < used ? before + n[0] : INT_MAX;
     }
-    bi_kv::launch_dependents();
+    __syncthreads();
+    if (tid < kItemRing)
+        sm.items[tid] = make_item(a, sm.first_chunk, sm.len, total, tid);
+    __syncthreads();
+    bi_kv::launch_dependents();   // the merge kernel's CTAs take the places that CTAs of this one leave
+    if (warp < kConsumers)
+        consume(sm, a, warp);
+    else if (warp < kConsumers + kHelpers)
+        help(sm, a, total, warp - kConsumers);
+    else
+        produce(sm, a, &k_map, &v_map);
 }
 
-// The chunks of one query head added in ascending order; sequences of one chunk are done already.
-// kSlices groups of D threads take consecutive runs of chunks, whose sums are then added in order.
+// The chunks of one query head added; sequences of one chunk are done already.  Warp w of the
+// head's kSlices takes the chunks w, w + kSlices, ... in ascending order, D / 32 dimensions a lane,
+// and the slices' sums are added in a fixed tree.  Latency bound: all parts a warp needs are in
+// flight at once for up to kBatch * kSlices chunks.
 constexpr int kSlices = 4;
+constexpr int kBatch = 8;
 
 template <int D>
-__global__ void __launch_bounds__(D * kSlices) paged_merge_kernel(const __grid_constant__ AttnArgs a)
+__global__ void __launch_bounds__(32 * kSlices) paged_merge_kernel(const __grid_constant__ AttnArgs a)
 {
-    __shared__ float2 ml_s[kMaxChunks];
-    __shared__ float acc_s[kSlices][D], sum_s[kSlices];
+    constexpr int kVec = D / 32;   // dimensions a lane
+    __shared__ float acc_s[kSlices][D], sum_s[kSlices], max_s[kSlices];
     const int64_t row = blockIdx.x;
     const int b = static_cast<int>(row / a.hq), h = static_cast<int>(row % a.hq);
-    const int tid = threadIdx.x, slice = tid / D, dd = tid % D;
+    const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
     bi_kv::dependency_wait();
-    const Span s = span_of(a.lens[b], a);
-    if (s.chunks == 1)
+    const int chunks = span_of(a.lens[b], a).chunks;
+    if (chunks == 1)
         return;
-    if (tid < s.chunks)
-        ml_s[tid] = a.part_ml[row * a.chunks + tid];
-    __syncthreads();
-    float mx = -INFINITY;
-    for (int c = 0; c < s.chunks; ++c)
-        mx = fmaxf(mx, ml_s[c].x);
-    const int per = (s.chunks + kSlices - 1) / kSlices;
-    const int lo = slice * per, hi = min(lo + per, s.chunks);
-    const float *part = a.part + row * a.chunks * D + dd;
-    float sum = 0.0f, acc = 0.0f;
-#pragma unroll 8
-    for (int c = lo; c < hi; ++c) {
-        const float f = exp2_approx(ml_s[c].x - mx);
-        sum = fmaf(ml_s[c].y, f, sum);
-        acc = fmaf(part[static_cast<int64_t>(c) * D], f, acc);
+    const float2 *ml = a.part_ml + row * a.chunks;
+    const float *part = a.part + row * a.chunks * D + lane * kVec;
+    float mx = -INFINITY, sum = 0.0f, acc[kVec] = {};
+    for (int c0 = slice; c0 < chunks; c0 += kSlices * kBatch) {
+        float v[kBatch][kVec];
+        float2 x[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int c = c0 + j * kSlices;
+            x[j] = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i)
+                v[j][i] = 0.0f;
+            if (c < chunks) {
+                x[j] = ml[c];
+                if constexpr (kVec == 4)
+                    *reinterpret_cast<float4 *>(v[j]) = *reinterpret_cast<const float4 *>(part + static_cast<int64_t>(c) * D);
+                else
+                    *reinterpret_cast<float2 *>(v[j]) = *reinterpret_cast<const float2 *>(part + static_cast<int64_t>(c) * D);
+            }
+        }
+        float top = mx;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+            top = fmaxf(top, x[j].x);
+        const float ref = top == -INFINITY ? 0.0f : top, old = exp2_approx(mx - ref);
+        sum *= old;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+            acc[i] *= old;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const float f = exp2_approx(x[j].x - ref);
+            sum = fmaf(x[j].y, f, sum);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i)
+                acc[i] = fmaf(v[j][i], f, acc[i]);
+        }
+        mx = top;
     }
-    acc_s[slice][dd] = acc;
-    if (dd == 0)
+    if (lane == 0) {
+        max_s[slice] = mx;
         sum_s[slice] = sum;
-    __syncthreads();
-    if (slice == 0) {
-        acc = (acc_s[0][dd] + acc_s[1][dd]) + (acc_s[2][dd] + acc_s[3][dd]);
-        sum = (sum_s[0] + sum_s[1]) + (sum_s[2] + sum_s[3]);
-        a.out[b * a.ldo + static_cast<int64_t>(h) * D + dd] = __float2bfloat16_rn(acc / sum);
-        if (a.lse && dd == 0)
-            a.lse[row] = (mx - kWeightExp + log2f(sum)) * kLn2;
     }
+#pragma unroll
+    for (int i = 0; i < kVec; ++i)
+        acc_s[slice][lane * kVec + i] = acc[i];
+    __syncthreads();
+    if (slice != 0)
+        return;
+    mx = fmaxf(fmaxf(max_s[0], max_s[1]), fmaxf(max_s[2], max_s[3]));
+    float f[kSlices];
+#pragma unroll
+    for (int s = 0; s < kSlices; ++s)
+        f[s] = exp2_approx(max_s[s] - mx);
+    sum = (sum_s[0] * f[0] + sum_s[1] * f[1]) + (sum_s[2] * f[2] + sum_s[3] * f[3]);
+    const float r = 1.0f / sum;
+    __nv_bfloat16 *out = a.out + b * a.ldo + static_cast<int64_t>(h) * D + lane * kVec;
+#pragma unroll
+    for (int i = 0; i < kVec; i += 2) {
+        float y[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int d = lane * kVec + i + j;
+            y[j] = (acc_s[0][d] * f[0] + acc_s[1][d] * f[1]) + (acc_s[2][d] * f[2] + acc_s[3][d] * f[3]);
+        }
+        *reinterpret_cast<__nv_bfloat162 *>(out + i) = __floats2bfloat162_rn(y[0] * r, y[1] * r);
+    }
+    if (a.lse && lane == 0)
+        a.lse[row] = (mx - kWeightExp + log2f(sum)) * kLn2;
 }
 
 // Chunks a sequence of up to max_len positions can have.
@@ -841,16 +893,17 @@ int64_t most_chunks(int64_t max_len)
     return steps < 1 ? 1 : steps < kMaxChunks ? steps : kMaxChunks;
 }
 
-template <int D, int NT>
-bi_status_t run_attention(const AttnArgs &a, int dev, int sms, cudaStream_t stream)
+template <int D, int MG>
+bi_status_t run_attention(const AttnArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map, int dev, int sms, cudaStream_t stream)
 {
     static std::mutex mu;
     static bool set[64] = {};
+    static_assert(sizeof(Shared<D, MG>) <= 232448, "shared memory of an SM");
     {
         std::lock_guard<std::mutex> lock(mu);
         if (!set[dev]) {
-            if (cudaFuncSetAttribute(paged_attention_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     static_cast<int>(sizeof(Shared<D, NT>))) != cudaSuccess) {
+            if (cudaFuncSetAttribute(paged_attention_kernel<D, MG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     static_cast<int>(sizeof(Shared<D, MG>))) != cudaSuccess) {
                 cudaGetLastError();
                 return BI_ERR_CUDA;
             }
@@ -860,10 +913,11 @@ bi_status_t run_attention(const AttnArgs &a, int dev, int sms, cudaStream_t stre
     // no more CTAs than there can be items
     const int64_t items = static_cast<int64_t>(a.b) * a.heads * a.chunks;
     const unsigned grid = static_cast<unsigned>(items < sms ? items : sms);
-    bi_status_t st = bi_kv::launch(paged_attention_kernel<D, NT>, dim3(grid), dim3(kThreads), sizeof(Shared<D, NT>), stream, 1, a);
+    bi_status_t st = bi_kv::launch(paged_attention_kernel<D, MG>, dim3(grid), dim3(kThreads), sizeof(Shared<D, MG>), stream, 1,
+                                  k_map, v_map, a);
     if (st != BI_OK || a.chunks == 1)
         return st;
-    return bi_kv::launch(paged_merge_kernel<D>, dim3(static_cast<unsigned>(a.b * a.hq)), dim3(D * kSlices), 0, stream, 1, a);
+    return bi_kv::launch(paged_merge_kernel<D>, dim3(static_cast<unsigned>(a.b * a.hq)), dim3(32 * kSlices), 0, stream, 1, a);
 }
 
 } // namespace
@@ -917,8 +971,6 @@ bi_status_t bi_paged_decode_attention(const bi_kv_cache_t *cache, const void *Q,
         return st;
     AttnArgs a = {};
     a.q = static_cast<const __nv_bfloat16 *>(Q);
-    a.k = static_cast<const uint8_t *>(cache->k);
-    a.v = static_cast<const uint8_t *>(cache->v);
     a.k_scale = cache->k_scale;
     a.v_scale = cache->v_scale;
     a.table = block_table;
@@ -928,9 +980,6 @@ bi_status_t bi_paged_decode_attention(const bi_kv_cache_t *cache, const void *Q,
     a.ldq = ldq;
     a.ldo = ldo;
     a.ld_table = ld_table;
-    a.page_stride = cache->page_stride;
-    a.token_stride = cache->token_stride;
-    a.head_stride = cache->head_stride;
     a.window = window;
     a.num_pages = static_cast<int>(cache->num_pages);
     a.max_len = static_cast<int>(max_len);
@@ -943,9 +992,15 @@ bi_status_t bi_paged_decode_attention(const bi_kv_cache_t *cache, const void *Q,
     a.scale = scale;
     a.part = static_cast<float *>(workspace);
     a.part_ml = reinterpret_cast<float2 *>(a.part + B * Hq * a.chunks * cache->head_dim);
+    CUtensorMap k_map, v_map;
+    if ((st = bi_kv::page_map(&k_map, cache, cache->k)) != BI_OK || (st = bi_kv::page_map(&v_map, cache, cache->v)) != BI_OK)
+        return st;
     if (cache->head_dim == 128)
-        return a.group <= 8 ? run_attention<128, 1>(a, dev, sms, stream) : run_attention<128, 2>(a, dev, sms, stream);
-    return a.group <= 8 ? run_attention<64, 1>(a, dev, sms, stream) : run_attention<64, 2>(a, dev, sms, stream);
+        return a.group <= 4   ? run_attention<128, 4>(a, k_map, v_map, dev, sms, stream)
+               : a.group <= 8 ? run_attention<128, 8>(a, k_map, v_map, dev, sms, stream)
+                              : run_attention<128, 16>(a, k_map, v_map, dev, sms, stream);
+    return a.group <= 8 ? run_attention<64, 8>(a, k_map, v_map, dev, sms, stream)
+                        : run_attention<64, 16>(a, k_map, v_map, dev, sms, stream);
 }
 
 } // extern "C"

@@ -41,6 +41,12 @@ def test_long_sequences(lens):
     check(Paged(lens, 1, 128, 64, seed=300 + lens[0]), 4, 1, 128, seed=3)
 
 
+@pytest.mark.parametrize("Hq,heads,D", [(16, 4, 128), (32, 4, 128), (32, 2, 128), (32, 4, 64), (32, 2, 64)])
+def test_long_chunks_of_many_heads(Hq, heads, D):
+    # chunks of several steps, more of them than CTAs, so that a CTA's two halves drift apart
+    check(Paged([30001, 20000, 70], heads, D, 128, seed=350 + Hq + D), Hq, heads, D, seed=3)
+
+
 @pytest.mark.parametrize("window", [1, 16, 17, 100, 256, 1000, 1 << 40])
 def test_windows(window):
     P = Paged([0, 1, 16, 17, 99, 100, 101, 255, 256, 257, 1000, 1001, 1500], 2, 128, 16, seed=400)
@@ -240,3 +246,17 @@ def test_large_batches():
     lens[::100] = 400
     P = Paged(lens, 1, 64, 16, seed=950)
     check(P, 2, 1, 64, seed=18)
+
+
+@pytest.mark.parametrize("heads,lens", [(8, [1500] * 700), (2, [5000, 1, 0, 300] * 450)])
+def test_many_items_per_block(heads, lens):
+    # hundreds of chunks for every resident block: their tables are refilled on the way.  All sequences
+    # of one length share their pages and queries, so their outputs are equal bit for bit.
+    distinct = sorted(set(lens))
+    P = Paged(distinct, heads, 64, 64, seed=960)
+    row = torch.tensor([distinct.index(n) for n in lens], device=DEV)
+    Q = queries(len(distinct), 2 * heads, 64, 19)
+    O, lse = attend(P.cache, Q[row].contiguous(), P.dtable[row].contiguous(), P.dlens[row].contiguous(), 0.125)
+    one, one_lse = attend(P.cache, Q, P.dtable, P.dlens, 0.125)
+    assert torch.equal(O.view(torch.int16), one.view(torch.int16)[row]) and torch.equal(lse, one_lse[row])
+    check(P, 2 * heads, heads, 64, seed=19, scale=0.125)

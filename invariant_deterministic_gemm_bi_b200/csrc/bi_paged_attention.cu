@@ -124,11 +124,12 @@ __device__ __forceinline__ Span span_of(int len, const AttnArgs &a)
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
 // one box of codes: positions [pos, pos + rows) of a page's head, all dimensions
-__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int pos, int head, int page)
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int pos, int head, int page, uint64_t policy)
 {
-    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
-                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(pos), "r"(head), "r"(page)
-                 : "memory");
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+                 " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;"
+                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(pos), "r"(head), "r"(page),
+                   "l"(policy) : "memory");
 }
 __device__ __forceinline__ void expect_bytes(uint64_t *bar, uint32_t bytes)
 {
@@ -325,6 +326,9 @@ __device__ __forceinline__ void produce(Shared<D, MG> &sm, const AttnArgs &a, co
     const int lane = threadIdx.x & 31, group = lane & 7, quarter = lane >> 3;
     const int box = a.page_shift == 4 ? 16 : kTile;   // positions of a TMA box
     const int page_mask = (1 << a.page_shift) - 1;
+    // codes are read once a call: marked first to leave L2 they do not push one another out before they
+    // arrive (64 x 4096, 32/8 heads: 92 us against 102 us without the mark)
+    const uint64_t policy = bi::ptx::policy_evict_first();
 
     // this lane's box of a block: whether any of it is attended, and its page
     struct Pages {
@@ -391,8 +395,8 @@ __device__ __forceinline__ void produce(Shared<D, MG> &sm, const AttnArgs &a, co
             __syncwarp();
             if (issue) {
                 const uint32_t dst = smem_u32(&sm.ring[slot][group >> 1][0][0]) + (group & 1) * 16 * D;
-                tma_box(dst, k_map, &sm.full[slot], px.key & page_mask, it.kvh, px.id);
-                tma_box(dst + S::kMatrix, v_map, &sm.full[slot], px.key & page_mask, it.kvh, px.id);
+                tma_box(dst, k_map, &sm.full[slot], px.key & page_mask, it.kvh, px.id, policy);
+                tma_box(dst + S::kMatrix, v_map, &sm.full[slot], px.key & page_mask, it.kvh, px.id, policy);
             }
             if (mine) {
                 // approximate to 2^-22: a page's weights are all off by one factor below 2^-21
@@ -795,102 +799,113 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_c
         produce(sm, a, &k_map, &v_map);
 }
 
-// The chunks of one query head added; sequences of one chunk are done already.  Warp w of the
-// head's kSlices takes the chunks w, w + kSlices, ... in ascending order, D / 32 dimensions a lane,
-// and the slices' sums are added in a fixed tree.  Latency bound: all parts a warp needs are in
-// flight at once for up to kBatch * kSlices chunks.
-constexpr int kSlices = 4;
-constexpr int kBatch = 8;
+// The chunks of one query head added; sequences of one chunk are done already.  Chunks are added
+// eight at a time in ascending order, and the eights in ascending order, so how many warps share
+// the eights of a head changes no bit: kWide warps, and kRows heads in a block.  Latency bound: a
+// warp has its eight parts in flight at once.
+constexpr int kEight = 8;
 
-template <int D>
-__global__ void __launch_bounds__(32 * kSlices) paged_merge_kernel(const __grid_constant__ AttnArgs a)
+template <int D, int kWide>
+__global__ void __launch_bounds__(kWide < 8 ? 256 : 32 * kWide) paged_merge_kernel(const __grid_constant__ AttnArgs a)
 {
+    constexpr int kRows = kWide < 8 ? 8 / kWide : 1;
     constexpr int kVec = D / 32;   // dimensions a lane
-    __shared__ float acc_s[kSlices][D], sum_s[kSlices], max_s[kSlices];
-    const int64_t row = blockIdx.x;
-    const int b = static_cast<int>(row / a.hq), h = static_cast<int>(row % a.hq);
-    const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+    constexpr int kEights = kWide == 1 ? 1 : kMaxChunks / kEight;
+    __shared__ float acc_s[kRows][kEights][D];
+    __shared__ float2 ml_s[kRows][kEights];
+    const int lane = threadIdx.x & 31, r = (threadIdx.x >> 5) / kWide, w = (threadIdx.x >> 5) % kWide;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + r;
     bi_kv::dependency_wait();
-    const int chunks = span_of(a.lens[b], a).chunks;
-    if (chunks == 1)
-        return;
-    const float2 *ml = a.part_ml + row * a.chunks;
-    const float *part = a.part + row * a.chunks * D + lane * kVec;
-    float mx = -INFINITY, sum = 0.0f, acc[kVec] = {};
-    for (int c0 = slice; c0 < chunks; c0 += kSlices * kBatch) {
-        float v[kBatch][kVec];
-        float2 x[kBatch];
+    const bool real = row < static_cast<int64_t>(a.b) * a.hq;
+    const int b = real ? static_cast<int>(row / a.hq) : 0;
+    const int chunks = real ? span_of(a.lens[b], a).chunks : 1;
+    const int eights = chunks == 1 ? 0 : (chunks + kEight - 1) / kEight;
+    for (int e = w; e < eights; e += kWide) {
+        const float2 *ml = a.part_ml + row * a.chunks + e * kEight;
+        const float *part = a.part + (row * a.chunks + e * kEight) * D + lane * kVec;
+        float v[kEight][kVec];
+        float2 x[kEight];
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            const int c = c0 + j * kSlices;
+        for (int j = 0; j < kEight; ++j) {
             x[j] = make_float2(-INFINITY, 0.0f);
 #pragma unroll
             for (int i = 0; i < kVec; ++i)
                 v[j][i] = 0.0f;
-            if (c < chunks) {
-                x[j] = ml[c];
+            if (e * kEight + j < chunks) {
+                x[j] = ml[j];
                 if constexpr (kVec == 4)
-                    *reinterpret_cast<float4 *>(v[j]) = *reinterpret_cast<const float4 *>(part + static_cast<int64_t>(c) * D);
+                    *reinterpret_cast<float4 *>(v[j]) = *reinterpret_cast<const float4 *>(part + j * D);
                 else
-                    *reinterpret_cast<float2 *>(v[j]) = *reinterpret_cast<const float2 *>(part + static_cast<int64_t>(c) * D);
+                    *reinterpret_cast<float2 *>(v[j]) = *reinterpret_cast<const float2 *>(part + j * D);
             }
         }
-        float top = mx;
+        float mx = -INFINITY, sum = 0.0f, acc[kVec] = {};
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-            top = fmaxf(top, x[j].x);
-        const float ref = top == -INFINITY ? 0.0f : top, old = exp2_approx(mx - ref);
-        sum *= old;
+        for (int j = 0; j < kEight; ++j)
+            mx = fmaxf(mx, x[j].x);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i)
-            acc[i] *= old;
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            const float f = exp2_approx(x[j].x - ref);
+        for (int j = 0; j < kEight; ++j) {
+            // a chunk of NaN scores has no maximum: its sum is NaN and stays so
+            const float f = exp2_approx(x[j].x - (mx == -INFINITY ? 0.0f : mx));
             sum = fmaf(x[j].y, f, sum);
 #pragma unroll
             for (int i = 0; i < kVec; ++i)
                 acc[i] = fmaf(v[j][i], f, acc[i]);
         }
-        mx = top;
-    }
-    if (lane == 0) {
-        max_s[slice] = mx;
-        sum_s[slice] = sum;
-    }
+        if (lane == 0)
+            ml_s[r][e] = make_float2(mx, sum);
 #pragma unroll
-    for (int i = 0; i < kVec; ++i)
-        acc_s[slice][lane * kVec + i] = acc[i];
-    __syncthreads();
-    if (slice != 0)
+        for (int i = 0; i < kVec; ++i)
+            acc_s[r][e][lane * kVec + i] = acc[i];
+    }
+    if constexpr (kWide > 1)
+        __syncthreads();
+    else
+        __syncwarp();
+    if (w != 0 || eights == 0)
         return;
-    mx = fmaxf(fmaxf(max_s[0], max_s[1]), fmaxf(max_s[2], max_s[3]));
-    float f[kSlices];
+    float mx = -INFINITY, sum = 0.0f, acc[kVec] = {};
+    for (int e = 0; e < eights; ++e)
+        mx = fmaxf(mx, ml_s[r][e].x);
+    for (int e = 0; e < eights; ++e) {
+        const float f = exp2_approx(ml_s[r][e].x - (mx == -INFINITY ? 0.0f : mx));
+        sum = fmaf(ml_s[r][e].y, f, sum);
 #pragma unroll
-    for (int s = 0; s < kSlices; ++s)
-        f[s] = exp2_approx(max_s[s] - mx);
-    sum = (sum_s[0] * f[0] + sum_s[1] * f[1]) + (sum_s[2] * f[2] + sum_s[3] * f[3]);
-    const float r = 1.0f / sum;
-    __nv_bfloat16 *out = a.out + b * a.ldo + static_cast<int64_t>(h) * D + lane * kVec;
-#pragma unroll
-    for (int i = 0; i < kVec; i += 2) {
-        float y[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int d = lane * kVec + i + j;
-            y[j] = (acc_s[0][d] * f[0] + acc_s[1][d] * f[1]) + (acc_s[2][d] * f[2] + acc_s[3][d] * f[3]);
-        }
-        *reinterpret_cast<__nv_bfloat162 *>(out + i) = __floats2bfloat162_rn(y[0] * r, y[1] * r);
+        for (int i = 0; i < kVec; ++i)
+            acc[i] = fmaf(acc_s[r][e][lane * kVec + i], f, acc[i]);
     }
+    const float inv = 1.0f / sum;
+    __nv_bfloat16 *out = a.out + b * a.ldo + (row - static_cast<int64_t>(b) * a.hq) * D + lane * kVec;
+#pragma unroll
+    for (int i = 0; i < kVec; i += 2)
+        *reinterpret_cast<__nv_bfloat162 *>(out + i) = __floats2bfloat162_rn(acc[i] * inv, acc[i + 1] * inv);
     if (a.lse && lane == 0)
         a.lse[row] = (mx - kWeightExp + log2f(sum)) * kLn2;
 }
 
-// Chunks a sequence of up to max_len positions can have.
+template <int D, int kWide>
+bi_status_t run_merge(const AttnArgs &a, cudaStream_t stream)
+{
+    constexpr int kRows = kWide < 8 ? 8 / kWide : 1;
+    const int64_t rows = static_cast<int64_t>(a.b) * a.hq;
+    return bi_kv::launch(paged_merge_kernel<D, kWide>, dim3(static_cast<unsigned>((rows + kRows - 1) / kRows)),
+                         dim3(32 * kWide * kRows), 0, stream, 1, a);
+}
+
+// The most chunks a sequence of up to max_len positions can have: chunk_steps() jumps at 4, 16 and
+// 512 steps, where the number of chunks falls.
 int64_t most_chunks(int64_t max_len)
 {
     const int64_t steps = (max_len + kStep - 1) / kStep;
-    return steps < 1 ? 1 : steps < kMaxChunks ? steps : kMaxChunks;
+    int64_t most = 1;
+    for (int64_t s : {INT64_C(4), INT64_C(16), INT64_C(4) * kMaxChunks, steps}) {
+        const int64_t n = s < steps ? s : steps;
+        if (n > 0) {
+            const int64_t per = chunk_steps(static_cast<int>(n)), chunks = (n + per - 1) / per;
+            most = chunks > most ? chunks : most;
+        }
+    }
+    return most;
 }
 
 template <int D, int MG>
@@ -917,7 +932,13 @@ bi_status_t run_attention(const AttnArgs &a, const CUtensorMap &k_map, const CUt
                                   k_map, v_map, a);
     if (st != BI_OK || a.chunks == 1)
         return st;
-    return bi_kv::launch(paged_merge_kernel<D>, dim3(static_cast<unsigned>(a.b * a.hq)), dim3(32 * kSlices), 0, stream, 1, a);
+    // Warps for a head: one where no sequence can have more than eight chunks; else four, or sixteen
+    // (all eights at once) while there are so few heads that all warps are resident (2 x 100001,
+    // 64 heads: 3.7 us against 11 us with four; 3200 ragged heads: 13 us against 8 us).
+    const int eights = (a.chunks + kEight - 1) / kEight;
+    return eights <= 1                                                            ? run_merge<D, 1>(a, stream)
+           : eights <= 4 || static_cast<int64_t>(a.b) * a.hq > INT64_C(4) * sms ? run_merge<D, 4>(a, stream)
+                                                                                  : run_merge<D, 16>(a, stream);
 }
 
 } // namespace

@@ -188,7 +188,8 @@ def _check(status: int, where: str):
 def _stream_handle(stream) -> int | None:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the handle of torch.cuda.current_stream(), without making a Stream object (3 us)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -501,38 +502,56 @@ def bi_quantize_e2m1(W, w_scale, Q, w_zero=None, stream=None):
 # Paged 8-bit key/value cache (include/bi_kv_cache.h, include/bi_paged_attention.h)
 # ---------------------------------------------------------------------------------------------
 
-def _on_current_device(*tensors):
-    """The C calls launch on the current device: a tensor of another one is refused here."""
-    import torch
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"every tensor must be on the current device cuda:{dev}")
+# A decode step makes these calls once a layer, so their checks are kept short: shapes and strides
+# are read once, and tensors of one kind go through one loop.
 
-
-def _int32_vectors(**tensors):
-    import torch
+def _require(device, dtype, **tensors):
+    """Every tensor (None is passed over) on the current device, contiguous and of the given type."""
     for name, t in tensors.items():
-        if t is not None and (t.dtype is not torch.int32 or not t.is_contiguous()):
-            raise TypeError(f"{name} must be a contiguous int32 tensor")
+        if t is not None:
+            if t.dtype is not dtype or not t.is_contiguous():
+                raise TypeError(f"{name} must be a contiguous {dtype} tensor")
+            if t.get_device() != device:
+                raise ValueError(f"{name} must be on the current device cuda:{device}")
 
 
-def _block_table(table):
+def _current_device() -> int:
+    """The current device's number; -1, the device number of CPU tensors' get_device(), without one
+    (argument checks then run to their end and the C call reports BI_ERR_NO_DEVICE)."""
     import torch
-    if table.dtype is not torch.int32 or table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
-        raise TypeError("block_table must be int32 [B, max_pages] with a unit inner stride")
-    # a one-row table's pitch is never used
-    return max(table.stride(0), table.shape[1])
+    try:
+        return torch.cuda.current_device()
+    except (AssertionError, RuntimeError):
+        return -1
 
 
-def _heads_rows(name, x, heads, dim):
-    """The row pitch of bf16 [rows, heads, dim] whose rows are contiguous (any pitch)."""
+def _heads_rows(name, x, device, heads, dim):
+    """(rows, row pitch) of bf16 [rows, heads, dim] whose rows are contiguous, of any pitch."""
     import torch
-    if x.dtype is not torch.bfloat16 or x.dim() != 3 or x.shape[1] != heads or x.shape[2] != dim:
-        raise TypeError(f"{name} must be bf16 [rows, {heads}, {dim}]")
-    if x.numel() and (x.stride(2) != 1 or (heads > 1 and x.stride(1) != dim)):
+    if x.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be bf16")
+    shape, stride = x.shape, x.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise TypeError(f"{name} must be [rows, {heads}, {dim}]")
+    rows = shape[0]
+    if rows and (stride[2] != 1 or (heads > 1 and stride[1] != dim)):
         raise TypeError(f"{name}: the {heads} x {dim} values of a row must be contiguous")
-    return x.stride(0) if x.shape[0] > 1 else heads * dim
+    if x.get_device() != device:
+        raise ValueError(f"{name} must be on the current device cuda:{device}")
+    return rows, (stride[0] if rows > 1 else heads * dim)
+
+
+def _block_table(table, device):
+    """(rows, width, row pitch) of a block table."""
+    import torch
+    if table.dtype is not torch.int32 or table.dim() != 2:
+        raise TypeError("block_table must be int32 [B, max_pages]")
+    (rows, width), stride = table.shape, table.stride()
+    if width > 1 and stride[1] != 1:
+        raise TypeError("block_table must have a unit inner stride")
+    if table.get_device() != device:
+        raise ValueError(f"block_table must be on the current device cuda:{device}")
+    return rows, width, (stride[0] if rows > 1 else width)
 
 
 class KvCache:
@@ -557,6 +576,7 @@ class KvCache:
             raise ValueError("the pools and their scales must be on one device")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.num_pages, self.page_size, self.num_heads, self.head_dim = k.shape
+        self.device = k.get_device()
         # the stride of an axis of one element is never used: give it the least that is valid
         ts = k.stride(1)
         hs = k.stride(2) if self.num_heads > 1 else self.head_dim
@@ -573,35 +593,38 @@ def bi_kv_block_tables(ctx_lens, new_lens, page_size: int, free_pages, free_coun
     ctx_lens, new_lens (-1: ended), seq_lens [B]; free_pages [capacity], a stack of free_count [1]
     pages; block_table [B, max_pages]; token_offsets [B+1]; slot_map, positions [max_tokens];
     free_left, status [1].  seq_lens may be ctx_lens and free_left may be free_count."""
-    B = ctx_lens.numel()
-    _int32_vectors(ctx_lens=ctx_lens, new_lens=new_lens, free_pages=free_pages, free_count=free_count,
-                   seq_lens=seq_lens, token_offsets=token_offsets, slot_map=slot_map, free_left=free_left,
-                   status=status, positions=positions)
-    ld = _block_table(block_table)
-    if new_lens.numel() != B or seq_lens.numel() != B or token_offsets.numel() != B + 1 or \
-            block_table.shape[0] != B or free_count.numel() != 1 or free_left.numel() != 1 or \
-            status.numel() != 1 or (positions is not None and positions.numel() != slot_map.numel()):
+    import torch
+    device = _current_device()
+    _require(device, torch.int32, ctx_lens=ctx_lens, new_lens=new_lens, free_pages=free_pages,
+             free_count=free_count, seq_lens=seq_lens, token_offsets=token_offsets, slot_map=slot_map,
+             free_left=free_left, status=status, positions=positions)
+    B, tokens = ctx_lens.numel(), slot_map.numel()
+    rows, width, ld = _block_table(block_table, device)
+    if rows != B or new_lens.numel() != B or seq_lens.numel() != B or token_offsets.numel() != B + 1 or \
+            free_count.numel() != 1 or free_left.numel() != 1 or status.numel() != 1 or \
+            (positions is not None and positions.numel() != tokens):
         raise ValueError("lengths of the arrays do not agree")
-    _on_current_device(ctx_lens, new_lens, free_pages, free_count, block_table, seq_lens, token_offsets,
-                       slot_map, free_left, status, positions)
     _check(load_library().bi_kv_block_tables(
-        _ptr(ctx_lens), _ptr(new_lens), B, page_size, _ptr(free_pages), free_pages.numel(), _ptr(free_count),
-        _ptr(block_table), ld, block_table.shape[1], _ptr(seq_lens), _ptr(token_offsets), _ptr(slot_map),
-        _ptr(positions), slot_map.numel(), _ptr(free_left), _ptr(status), _stream_handle(stream)),
-        "bi_kv_block_tables")
+        ctx_lens.data_ptr(), new_lens.data_ptr(), B, page_size, free_pages.data_ptr(), free_pages.numel(),
+        free_count.data_ptr(), block_table.data_ptr(), ld, width, seq_lens.data_ptr(),
+        token_offsets.data_ptr(), slot_map.data_ptr(), _ptr(positions), tokens, free_left.data_ptr(),
+        status.data_ptr(), _stream_handle(stream)), "bi_kv_block_tables")
 
 
 def bi_kv_append_e4m3(cache: KvCache, K, V, slot_map, stream=None):
     """Write bf16 K, V [T, heads, head_dim] (rows of any pitch) to the slots slot_map int32 [T]."""
-    T = K.shape[0]
-    if V.shape[0] != T or slot_map.numel() != T:
+    import torch
+    device = _current_device()
+    T, ldk = _heads_rows("K", K, device, cache.num_heads, cache.head_dim)
+    rows, ldv = _heads_rows("V", V, device, cache.num_heads, cache.head_dim)
+    _require(device, torch.int32, slot_map=slot_map)
+    if rows != T or slot_map.numel() != T:
         raise ValueError("K, V and slot_map must have the same number of rows")
-    ldk = _heads_rows("K", K, cache.num_heads, cache.head_dim)
-    ldv = _heads_rows("V", V, cache.num_heads, cache.head_dim)
-    _int32_vectors(slot_map=slot_map)
-    _on_current_device(cache.k, K, V, slot_map)
-    _check(load_library().bi_kv_append_e4m3(cache.ref, _ptr(K), ldk, _ptr(V), ldv, _ptr(slot_map), T,
-                                            _stream_handle(stream)), "bi_kv_append_e4m3")
+    if cache.device != device:
+        raise ValueError(f"the cache must be on the current device cuda:{device}")
+    _check(load_library().bi_kv_append_e4m3(cache.ref, K.data_ptr(), ldk, V.data_ptr(), ldv,
+                                            slot_map.data_ptr(), T, _stream_handle(stream)),
+           "bi_kv_append_e4m3")
 
 
 def bi_paged_decode_attention_workspace_bytes(B: int, Hq: int, D: int, max_len: int) -> int:
@@ -611,22 +634,29 @@ def bi_paged_decode_attention_workspace_bytes(B: int, Hq: int, D: int, max_len: 
 def bi_paged_decode_attention(cache: KvCache, Q, block_table, seq_lens, O, scale: float, workspace=None,
                               lse=None, window: int = 0, stream=None):
     """Q [B, Hq, D] bf16, block_table int32 [B, max_pages], seq_lens int32 [B] -> O [B, Hq, D] bf16
-    and, if given, lse fp32 [B, Hq].  workspace: a device tensor of at least
+    and, if given, lse fp32 [B, Hq].  workspace: a contiguous device tensor of at least
     bi_paged_decode_attention_workspace_bytes(B, Hq, D, max_pages * page_size) bytes."""
     import torch
-    B, Hq = Q.shape[0], Q.shape[1]
-    ldq = _heads_rows("Q", Q, Hq, cache.head_dim)
-    ldo = _heads_rows("O", O, Hq, cache.head_dim)
-    ld = _block_table(block_table)
-    _int32_vectors(seq_lens=seq_lens)
-    if O.shape[0] != B or block_table.shape[0] != B or seq_lens.numel() != B:
+    device = _current_device()
+    Hq = Q.shape[1]
+    B, ldq = _heads_rows("Q", Q, device, Hq, cache.head_dim)
+    rows, ldo = _heads_rows("O", O, device, Hq, cache.head_dim)
+    table_rows, width, ld = _block_table(block_table, device)
+    _require(device, torch.int32, seq_lens=seq_lens)
+    if rows != B or table_rows != B or seq_lens.numel() != B:
         raise ValueError("Q, O, block_table and seq_lens must have the same number of rows")
-    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (B, Hq) or not lse.is_contiguous()):
-        raise TypeError("lse must be contiguous fp32 [B, Hq]")
-    _on_current_device(cache.k, Q, block_table, seq_lens, O, workspace, lse)
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if lse is not None:
+        _require(device, torch.float32, lse=lse)
+        if lse.shape != (B, Hq):
+            raise TypeError("lse must be [B, Hq]")
+    nbytes = 0
+    if workspace is not None:
+        _require(device, workspace.dtype, workspace=workspace)
+        nbytes = workspace.numel() * workspace.element_size()
+    if cache.device != device:
+        raise ValueError(f"the cache must be on the current device cuda:{device}")
     _check(load_library().bi_paged_decode_attention(
-        cache.ref, _ptr(Q), ldq, _ptr(block_table), ld, block_table.shape[1], _ptr(seq_lens), B, Hq, scale,
-        window, _ptr(workspace), nbytes, _ptr(O), ldo, _ptr(lse), _stream_handle(stream)),
+        cache.ref, Q.data_ptr(), ldq, block_table.data_ptr(), ld, width, seq_lens.data_ptr(), B, Hq, scale,
+        window, _ptr(workspace), nbytes, O.data_ptr(), ldo, _ptr(lse), _stream_handle(stream)),
         "bi_paged_decode_attention")
     return O

@@ -6,7 +6,8 @@
 //
 // Work.  A sequence's positions are cut into steps of 256 at multiples of 256, and runs of steps
 // into chunks whose length follows from the number of steps alone.  An item is one chunk of one
-// key/value head; persistent CTAs take items round robin.  Consumer warp w of a CTA owns positions
+// key/value head; persistent CTAs take items round robin, those of long chunks first so that short
+// ones fill the gaps at the end.  Consumer warp w of a CTA owns positions
 // 32 w .. 32 w + 31 of every step and keeps a softmax state of its own over the chunk; the eight
 // states are added in warp order at the chunk's end, and the chunks in ascending order by a second
 // kernel.  Every sum's order is thus fixed by the sequence's length and window.
@@ -62,6 +63,7 @@ constexpr int kStep = kConsumers * kTile;   // positions of a CTA's step
 constexpr int kMaxChunks = 128;             // chunks of a sequence
 constexpr int kMaxGroup = 16;               // query heads of a key/value head
 constexpr int kEntries = 512;               // entries of the scanned chunk counts
+constexpr int kClasses = 3;                 // of sequences, by steps per chunk: 4 and more, 2, 1
 constexpr int kItemBlock = 32;              // items whose table entries one warp makes at once
 constexpr int kItemRing = 4 * kItemBlock;   // entries of the items' table
 constexpr int kMaxBatch = kEntries * 32;    // an entry stands for up to 32 sequences
@@ -102,6 +104,8 @@ struct Span {
     int lo, hi, first, steps, per_chunk, chunks;
     bool bad;
 };
+
+__host__ __device__ __forceinline__ int class_of(int per_chunk) { return per_chunk >= 4 ? 0 : per_chunk == 2 ? 1 : 2; }
 
 __device__ __forceinline__ Span span_of(int len, const AttnArgs &a)
 {
@@ -237,9 +241,10 @@ struct Shared {
     // A chunk's states are written; the helpers have read the states of the item before and prepared
     // the queries of the one after (even and odd items apart: the helpers may be one ahead).
     uint64_t states, helped[2];
-    int32_t first_chunk[kEntries];                          // chunks before each entry
+    int32_t first_chunk[kClasses][kEntries];                // chunks of the class before each entry
+    int32_t class_chunks[kClasses];
     int32_t len[kEntries];                                  // lengths, when an entry is one sequence
-    int32_t warp_sum[kThreads / 32];
+    int32_t warp_sum[kClasses][kThreads / 32];
     int dead;                                               // a wait gave up
 };
 
@@ -274,32 +279,37 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar)
         bi::ptx::mbar_arrive(bar);
 }
 
-// Item number i of this CTA: chunk ordinal u of the scan and a key/value head, one lane an item.
-__device__ __forceinline__ Item make_item(const AttnArgs &a, const int32_t *first_chunk, const int32_t *len_s, int total, int i)
+// Item number i of this CTA, one lane an item: chunk ordinal u of the classes in order, and a
+// key/value head.
+template <typename S>
+__device__ __forceinline__ Item make_item(const AttnArgs &a, const S &sm, int i)
 {
     Item it = {};
     const int64_t n = blockIdx.x + static_cast<int64_t>(i) * gridDim.x;
     it.b = -1;
-    if (n >= static_cast<int64_t>(total) * a.heads)
+    const int most = sm.class_chunks[0] + sm.class_chunks[1] + sm.class_chunks[2];
+    if (n >= static_cast<int64_t>(most) * a.heads)
         return it;
-    const int u = static_cast<int>(n / a.heads);
-    it.kvh = static_cast<int>(n - static_cast<int64_t>(u) * a.heads);
-    int e = 0;   // the last entry with first_chunk <= u
+    int chunk = static_cast<int>(n) / a.heads;
+    it.kvh = static_cast<int>(n) - chunk * a.heads;
+    int cls = 0;
+    while (chunk >= sm.class_chunks[cls])
+        chunk -= sm.class_chunks[cls++];
+    const int32_t *first_chunk = sm.first_chunk[cls];
+    int e = 0;   // the last entry with first_chunk <= chunk
 #pragma unroll
     for (int step = kEntries / 2; step > 0; step >>= 1)
-        if (first_chunk[e + step] <= u)
+        if (first_chunk[e + step] <= chunk)
             e += step;
-    int chunk = u - first_chunk[e], b = e;
+    chunk -= first_chunk[e];
+    int b = e;
     Span s;
     if (a.b <= kEntries) {
-        s = span_of(len_s[b], a);
-    } else {   // an entry is several consecutive sequences
+        s = span_of(sm.len[b], a);
+    } else {   // an entry is several consecutive sequences, of which those of the class count
         b = e * ((a.b + kEntries - 1) / kEntries);
-        s = span_of(a.lens[b], a);
-        while (chunk >= s.chunks) {
-            chunk -= s.chunks;
-            s = span_of(a.lens[++b], a);
-        }
+        for (s = span_of(a.lens[b], a); class_of(s.per_chunk) != cls || chunk >= s.chunks; s = span_of(a.lens[++b], a))
+            chunk -= class_of(s.per_chunk) == cls ? s.chunks : 0;
     }
     it.b = b;
     it.lo = s.lo;
@@ -693,7 +703,7 @@ __device__ __forceinline__ void add_states(Shared<D, MG> &sm, const AttnArgs &a,
 }
 
 template <int D, int MG>
-__device__ __forceinline__ void help(Shared<D, MG> &sm, const AttnArgs &a, int total, int w)
+__device__ __forceinline__ void help(Shared<D, MG> &sm, const AttnArgs &a, int w)
 {
     for (int i = 0; i < 2; ++i) {
         const Item it = sm.items[i];
@@ -715,7 +725,7 @@ __device__ __forceinline__ void help(Shared<D, MG> &sm, const AttnArgs &a, int t
         // before), and the other warps read the new entries behind the barriers of the items between.
         if (w == 0 && i > 0 && i % kItemBlock == 0) {
             const int lane = threadIdx.x & 31, first = i - kItemBlock;
-            sm.items[(first + lane) % kItemRing] = make_item(a, sm.first_chunk, sm.len, total, first + kItemRing + lane);
+            sm.items[(first + lane) % kItemRing] = make_item(a, sm, first + kItemRing + lane);
         }
         warp_arrive(&sm.helped[i & 1]);
     }
@@ -749,10 +759,10 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_c
         (&sm.qc[0][0])[tid] = 0.0f;
     bi_kv::dependency_wait();
 
-    // chunks before each entry: thread i scans entries 2 i and 2 i + 1
+    // chunks before each entry, class by class: thread i scans entries 2 i and 2 i + 1
     const int per = (a.b + kEntries - 1) / kEntries;
     static_assert(2 * kThreads >= kEntries, "two entries a thread");
-    int n[2] = {0, 0};
+    int n[2][kClasses] = {}, incl[kClasses];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int e = 2 * tid + j;
@@ -761,40 +771,51 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_c
                 const int len = a.lens[b];
                 if (per == 1)
                     sm.len[e] = len;
-                n[j] += span_of(len, a).chunks;
+                const Span s = span_of(len, a);
+#pragma unroll
+                for (int c = 0; c < kClasses; ++c)
+                    n[j][c] += class_of(s.per_chunk) == c ? s.chunks : 0;
             }
     }
-    int incl = n[0] + n[1];
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int y = __shfl_up_sync(kFull, incl, off);
-        if (lane >= off)
-            incl += y;
+    for (int c = 0; c < kClasses; ++c) {
+        incl[c] = n[0][c] + n[1][c];
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(kFull, incl[c], off);
+            if (lane >= off)
+                incl[c] += y;
+        }
+        if (lane == 31)
+            sm.warp_sum[c][warp] = incl[c];
     }
-    if (lane == 31)
-        sm.warp_sum[warp] = incl;
     __syncthreads();
-    int before = incl - n[0] - n[1], total = 0;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        before += w < warp ? sm.warp_sum[w] : 0;
-        total += sm.warp_sum[w];
-    }
-    // entries behind the last sequence hold INT_MAX
-    const int used = (a.b + per - 1) / per;
-    if (2 * tid < kEntries) {
-        sm.first_chunk[2 * tid] = 2 * tid < used ? before : INT_MAX;
-        sm.first_chunk[2 * tid + 1] = 2 * tid + 1 < used ? before + n[0] : INT_MAX;
+    for (int c = 0; c < kClasses; ++c) {
+        int before = incl[c] - n[0][c] - n[1][c], total = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            before += w < warp ? sm.warp_sum[c][w] : 0;
+            total += sm.warp_sum[c][w];
+        }
+        // entries behind the last sequence hold INT_MAX
+        const int used = (a.b + per - 1) / per;
+        if (2 * tid < kEntries) {
+            sm.first_chunk[c][2 * tid] = 2 * tid < used ? before : INT_MAX;
+            sm.first_chunk[c][2 * tid + 1] = 2 * tid + 1 < used ? before + n[0][c] : INT_MAX;
+        }
+        if (tid == 0)
+            sm.class_chunks[c] = total;
     }
     __syncthreads();
     if (tid < kItemRing)
-        sm.items[tid] = make_item(a, sm.first_chunk, sm.len, total, tid);
+        sm.items[tid] = make_item(a, sm, tid);
     __syncthreads();
     bi_kv::launch_dependents();   // the merge kernel's CTAs take the places that CTAs of this one leave
     if (warp < kConsumers)
         consume(sm, a, warp);
     else if (warp < kConsumers + kHelpers)
-        help(sm, a, total, warp - kConsumers);
+        help(sm, a, warp - kConsumers);
     else
         produce(sm, a, &k_map, &v_map);
 }

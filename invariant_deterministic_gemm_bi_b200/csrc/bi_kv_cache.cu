@@ -201,14 +201,17 @@ __global__ void __launch_bounds__(kTableThreads, 1) kv_tables_kernel(TableArgs a
 }
 
 // ---------------------------------------------------------------------------------------------
-// The write into the cache.  A run -- rows with consecutive slots of one page -- belongs to the
-// CTA that owns its first row; it takes one head of K or of V.  The new exponent is the maximum of
-// the page's old one and the run's, so one pass over the run finds it and a second one (from L1)
-// rounds and stores; only when the exponent grows are the page's earlier codes read and moved.
-// Memory bound for prompts, latency bound for a decode step.
+// The write into the cache.  A run -- rows with consecutive slots of one page -- has at most
+// page_size tokens; a group of page_size / 32 warps (one for pages of 16) takes one head of K or of V
+// and the runs that begin in a block of rows, 32 tokens of a run a warp, which stay in registers
+// between the pass that finds the largest magnitude and the one that rounds.  Only when a page's
+// exponent grows are its earlier codes read and moved.  The warps of a CTA take neighbouring heads,
+// whose rows lie side by side.  Memory bound for prompts (8 prompts, 9.4k tokens, 8 heads of 128:
+// one pass, 6 bytes a value), latency bound for a decode step.
 // ---------------------------------------------------------------------------------------------
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendWarps = 8;
+constexpr int kPiece = 32;   // tokens of a run one warp holds
 
 struct AppendArgs {
     const __nv_bfloat16 *x[2];   // K, V
@@ -246,66 +249,135 @@ __device__ __forceinline__ int exponent_of(uint32_t amax_bits)
     return max(bi_kv::kScaleExpMin, min(bi_kv::kScaleExpMax, e));
 }
 
-__device__ __forceinline__ uint32_t amax2(uint32_t best, uint32_t pair)
+// Magnitudes of two bf16 at or above this round up to infinity at 4 significant bits, or are not finite.
+constexpr uint32_t kHuge = 0x7f78u;
+
+// R(x * inv) of two bf16 values below kHuge, as two e4m3 bytes.  Rounding to 4 significant bits
+// works on the bf16 bits of both at once (dividing by a power of two changes no significant bit).
+// Cutting to a multiple of 2^-9 changes no value of 4 significant bits from 2^-6 on, so it needs no
+// case: with c = +-2^14, whose unit in the last place is 2^-9, (x inv + c, cut) - c is the cut.
+__device__ __forceinline__ uint32_t codes_of(uint32_t two, float inv)
 {
-    const uint32_t lo = pair & 0x7fffu, hi = (pair >> 16) & 0x7fffu;
+    const uint32_t r = (two + 0x00070007u + ((two >> 4) & 0x00010001u)) & 0xfff0fff0u;
+    const float lo = __uint_as_float(r << 16), hi = __uint_as_float(r & 0xffff0000u);
+    const float c_lo = copysignf(16384.0f, lo), c_hi = copysignf(16384.0f, hi);
+    // a value cut to zero keeps its sign, as in code_of
+    const float y_lo = copysignf(__fmaf_rz(lo, inv, c_lo) - c_lo, lo), y_hi = copysignf(__fmaf_rz(hi, inv, c_hi) - c_hi, hi);
+    uint16_t y;
+    // exact for every value up to 448; saturates above
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(y) : "f"(y_hi), "f"(y_lo));
+    return y;
+}
+
+// Largest of two bf16 magnitudes so far and in a word, packed.
+__device__ __forceinline__ uint32_t magnitudes(uint32_t best, uint32_t two) { return __vmaxu2(best, two & 0x7fff7fffu); }
+__device__ __forceinline__ uint32_t finite_magnitude(uint32_t best, uint32_t two)
+{
+    const uint32_t lo = two & 0x7fffu, hi = (two >> 16) & 0x7fffu;
     best = lo < 0x7f80u ? max(best, lo) : best;
     return hi < 0x7f80u ? max(best, hi) : best;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendArgs a)
+// One group's warps (G of them, named barrier 1 + group); nothing to wait for in a group of one.
+template <int G>
+__device__ __forceinline__ void group_sync(int group)
 {
-    constexpr int kVecs = D / 8;   // 16-byte vectors of a row's head
-    __shared__ uint32_t red[kAppendThreads / 32];
-    __shared__ int run_end;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int h = blockIdx.y, kv = blockIdx.z;
+    if constexpr (G > 1)
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(32 * G) : "memory");
+}
+
+template <int D, int G>
+__global__ void __launch_bounds__(32 * kAppendWarps) kv_append_kernel(const __grid_constant__ AppendArgs a)
+{
+    constexpr int kVecs = D / 8;             // 16-byte vectors of a row's head
+    constexpr int kTokens = 32 / kVecs;      // tokens one load instruction covers
+    constexpr int kLoads = kPiece / kTokens;
+    __shared__ uint32_t top_s[2][kAppendWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int group = warp / G, part = warp % G;
     const int page = 1 << a.page_shift;
     bi_kv::dependency_wait();
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * a.rows;
-    const int64_t last = min(first + a.rows, static_cast<int64_t>(a.t));
-    for (int64_t t = first; t < last; ++t) {   // uniform over the CTA
-        const int64_t slot = a.slots[t];
-        if (slot < 0 || slot >= a.num_slots)
-            continue;
+    // unit: a block of rows, K or V, a head
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kAppendWarps / G) + group;
+    const int h = static_cast<int>(unit % a.heads), kv = static_cast<int>(unit / a.heads % 2);
+    const int64_t t0 = unit / a.heads / 2 * a.rows;
+    if (t0 >= a.t)
+        return;
+    const __nv_bfloat16 *x = a.x[kv] + static_cast<int64_t>(h) * D + (lane % kVecs) * 8;
+    const int64_t ld = a.ld[kv];
+
+    // the block's rows, one a lane; a run begins where a row does not continue the one before
+    const int64_t t = t0 + lane;
+    const int64_t mine = lane < a.rows && t < a.t ? a.slots[t] : -1;
+    const bool valid = mine >= 0 && mine < a.num_slots;
+    const bool follows = valid && (mine & (page - 1)) != 0 && t > 0 && a.slots[t - 1] == mine - 1;
+    const uint32_t follow = __ballot_sync(kFull, follows);
+    uint32_t first = __ballot_sync(kFull, valid && !follows);
+    for (int run = 0; first != 0; ++run) {
+        const int i = __ffs(first) - 1;
+        first &= first - 1;
+        const int64_t row0 = t0 + i, slot = __shfl_sync(kFull, static_cast<int>(mine), i);
         const int off = static_cast<int>(slot & (page - 1));
-        if (off != 0 && t > 0 && a.slots[t - 1] == slot - 1)
-            continue;   // inside a run
-        // the run's length: rows t + i with slot + i, up to the page's end
-        if (tid == 0)
-            run_end = static_cast<int>(min(static_cast<int64_t>(page - off), a.t - t));
-        __syncthreads();
-        if (tid < page - off && t + tid < a.t && a.slots[t + tid] != slot + tid)
-            atomicMin(&run_end, tid);
-        __syncthreads();
-        const int n = run_end;
-        const __nv_bfloat16 *x = a.x[kv] + t * a.ld[kv] + static_cast<int64_t>(h) * D;
-        uint32_t amax = 0;
-        for (int i = tid; i < n * kVecs; i += kAppendThreads) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(x + (i / kVecs) * a.ld[kv]) + i % kVecs);
-            amax = amax2(amax2(amax2(amax2(amax, v.x), v.y), v.z), v.w);
-        }
-        amax = __reduce_max_sync(kFull, amax);
-        if (lane == 0)
-            red[warp] = amax;
-        __syncthreads();
+        const int most = static_cast<int>(min(static_cast<int64_t>(page - off), a.t - row0));
+        int n = __ffs(~(static_cast<uint32_t>(static_cast<uint64_t>(follow) >> (i + 1))));   // 1 + the rows that follow
+        n = n == 0 ? 32 : n;
+        if (n >= a.rows - i)   // to the block's end: look on
+            for (n = a.rows - i; n < most;) {
+                const int64_t at = row0 + n + lane;
+                const uint32_t on = __ballot_sync(kFull, n + lane < most && a.slots[at] == slot + n + lane);
+                const int more = on == kFull ? 32 : __ffs(~on) - 1;
+                n += more;
+                if (more < 32)
+                    break;
+            }
+        n = min(n, most);
+
+        // this warp's tokens of the run
+        const int begin = part * kPiece, count = min(n - begin, kPiece);
+        uint4 v[kLoads];
+        uint32_t best = 0;
 #pragma unroll
-        for (int w = 0; w < kAppendThreads / 32; ++w)
-            amax = max(amax, red[w]);
+        for (int j = 0; j < kLoads; ++j) {
+            const int tok = j * kTokens + lane / kVecs;
+            v[j] = make_uint4(0, 0, 0, 0);
+            if (tok < count)
+                v[j] = __ldg(reinterpret_cast<const uint4 *>(x + (row0 + begin + tok) * ld));
+        }
         const int64_t p = slot >> a.page_shift;
         float *scale = a.scale[kv] + p * a.heads + h;
         uint8_t *codes = a.codes[kv] + p * a.page_stride + h * a.head_stride;
-        int e = exponent_of(amax);
+        const uint32_t old_scale = off != 0 ? __float_as_uint(*scale) : 0;
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j)
+            best = magnitudes(magnitudes(magnitudes(magnitudes(best, v[j].x), v[j].y), v[j].z), v[j].w);
+        uint32_t top = max(best & 0xffffu, best >> 16);
+        const bool huge = top >= kHuge;   // this lane holds one
+        if (huge) {
+            top = 0;
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j)
+                top = finite_magnitude(finite_magnitude(finite_magnitude(finite_magnitude(top, v[j].x), v[j].y), v[j].z), v[j].w);
+        }
+        top = __reduce_max_sync(kFull, top);
+        if constexpr (G > 1) {
+            if (lane == 0)
+                top_s[run & 1][warp] = top;
+            group_sync<G>(group);   // also: every warp has read the scale
+#pragma unroll
+            for (int w = 0; w < G; ++w)
+                top = max(top, top_s[run & 1][group * G + w]);
+        }
+        int e = exponent_of(top);
         if (off != 0) {
-            int old = static_cast<int>((__float_as_uint(*scale) >> 23) & 0xffu) - 127;
+            int old = static_cast<int>((old_scale >> 23) & 0xffu) - 127;
             old = max(bi_kv::kScaleExpMin, min(bi_kv::kScaleExpMax, old));
             if (e > old) {   // the earlier codes move to the new scale
                 const float f = pow2(max(old - e, -126));
-                for (int i = tid; i < off * (D / 16); i += kAppendThreads) {
-                    uint4 *at = reinterpret_cast<uint4 *>(codes + (i / (D / 16)) * a.token_stride) + i % (D / 16);
-                    uint4 v = *at;
-                    uint32_t *w = reinterpret_cast<uint32_t *>(&v);
+                const int end = min(off, begin + kPiece);
+                for (int y = begin * (D / 16) + lane; y < end * (D / 16); y += 32) {
+                    uint4 *at = reinterpret_cast<uint4 *>(codes + (y / (D / 16)) * a.token_stride) + y % (D / 16);
+                    uint4 q = *at;
+                    uint32_t *w = reinterpret_cast<uint32_t *>(&q);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         uint32_t out = 0;
@@ -317,31 +389,45 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendArgs a)
                         }
                         w[j] = out;
                     }
-                    *at = v;
+                    *at = q;
                 }
             } else {
                 e = old;
             }
         }
-        __syncthreads();   // everyone has read the scale
-        if (tid == 0)
+        if (part == 0 && lane == 0)
             *scale = pow2(e);
         const float inv = pow2(-e);
-        for (int i = tid; i < n * kVecs; i += kAppendThreads) {
-            const int row = i / kVecs, vec = i % kVecs;
-            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(x + row * a.ld[kv]) + vec);
-            const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-            uint32_t out[2] = {0, 0};
+        uint8_t *to = codes + (off + begin) * a.token_stride + (lane % kVecs) * 8;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t lo = code_of(__uint_as_float(in[j] << 16) * inv);
-                const uint32_t hi = code_of(__uint_as_float(in[j] & 0xffff0000u) * inv);
-                out[j >> 1] |= (lo | (hi << 8)) << (16 * (j & 1));
+        for (int j = 0; j < kLoads; ++j) {
+            const int tok = j * kTokens + lane / kVecs;
+            if (tok < count) {
+                const uint32_t in[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+                uint32_t out[4];
+                if (!huge) {
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        out[y] = codes_of(in[y], inv);
+                } else {
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        out[y] = code_of(__uint_as_float(in[y] << 16) * inv) |
+                                 (code_of(__uint_as_float(in[y] & 0xffff0000u) * inv) << 8);
+                }
+                *reinterpret_cast<uint2 *>(to + tok * a.token_stride) =
+                    make_uint2(out[0] | (out[1] << 16), out[2] | (out[3] << 16));
             }
-            *reinterpret_cast<uint2 *>(codes + (off + row) * a.token_stride + vec * 8) = make_uint2(out[0], out[1]);
         }
-        __syncthreads();   // the shared words are free for the next run
     }
+}
+
+template <int D, int G>
+bi_status_t run_append(const AppendArgs &a, int64_t blocks_of_rows, cudaStream_t stream)
+{
+    const int64_t units = blocks_of_rows * 2 * a.heads, per = kAppendWarps / G;
+    return bi_kv::launch(kv_append_kernel<D, G>, dim3(static_cast<unsigned>((units + per - 1) / per)), dim3(32 * kAppendWarps), 0,
+                         stream, 1, a);
 }
 
 } // namespace
@@ -439,15 +525,25 @@ bi_status_t bi_kv_append_e4m3(const bi_kv_cache_t *cache, const void *K, int64_t
     a.t = static_cast<int>(T);
     a.heads = cache->num_heads;
     a.page_shift = bi_kv::log2_of(cache->page_size);
-    // rows per CTA: 1 while that gives no more than 16 CTAs per SM, at most 32
-    const int64_t per_row = 2 * static_cast<int64_t>(cache->num_heads);
+    // Rows per block: one, so that the runs of a decode step are written side by side, until that
+    // gives more than 32 groups per SM; at most a warp's 32.
+    const int64_t groups = 2 * static_cast<int64_t>(cache->num_heads);
     a.rows = 1;
-    while (a.rows < 32 && (T + a.rows - 1) / a.rows * per_row > 16 * static_cast<int64_t>(sms))
+    while (a.rows < 32 && (T + a.rows - 1) / a.rows * groups > 32 * static_cast<int64_t>(sms))
         a.rows *= 2;
-    const dim3 grid(static_cast<unsigned>((T + a.rows - 1) / a.rows), cache->num_heads, 2);
-    return cache->head_dim == 128
-               ? bi_kv::launch(kv_append_kernel<128>, grid, dim3(kAppendThreads), 0, stream, 1, a)
-               : bi_kv::launch(kv_append_kernel<64>, grid, dim3(kAppendThreads), 0, stream, 1, a);
+    const int64_t blocks = (T + a.rows - 1) / a.rows;
+    if (blocks > INT32_MAX / groups)
+        return BI_ERR_UNSUPPORTED_SHAPE;
+    const int warps = cache->page_size <= kPiece ? 1 : cache->page_size / kPiece;
+    if (cache->head_dim == 128)
+        return warps == 1   ? run_append<128, 1>(a, blocks, stream)
+               : warps == 2 ? run_append<128, 2>(a, blocks, stream)
+               : warps == 4 ? run_append<128, 4>(a, blocks, stream)
+                            : run_append<128, 8>(a, blocks, stream);
+    return warps == 1   ? run_append<64, 1>(a, blocks, stream)
+           : warps == 2 ? run_append<64, 2>(a, blocks, stream)
+           : warps == 4 ? run_append<64, 4>(a, blocks, stream)
+                        : run_append<64, 8>(a, blocks, stream);
 }
 
 } // extern "C"

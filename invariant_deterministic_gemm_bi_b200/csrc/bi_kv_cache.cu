@@ -1,6 +1,7 @@
 // bi_kv_cache.cu -- the paged 8-bit cache's block tables and the write into it
 // (include/bi_kv_cache.h).
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
@@ -210,8 +211,9 @@ __global__ void __launch_bounds__(kTableThreads, 1) kv_tables_kernel(TableArgs a
 // one pass, 6 bytes a value), latency bound for a decode step.
 // ---------------------------------------------------------------------------------------------
 
-constexpr int kAppendWarps = 8;
 constexpr int kPiece = 32;   // tokens of a run one warp holds
+template <int G>
+constexpr int kAppendWarpsOf = G > 8 ? G : 8;
 
 struct AppendArgs {
     const __nv_bfloat16 *x[2];   // K, V
@@ -228,7 +230,7 @@ __device__ __forceinline__ uint32_t code_of(float y)
 {
     const uint32_t bits = __float_as_uint(y);
     if ((bits & 0x7fffffffu) >= 0x7f800000u)
-        return 0x7fu | ((bits >> 24) & 0x80u);   // infinity and NaN: NaN
+        return 0x7fu;                            // infinity and NaN: NaN
     // nearest even at 4 significant bits (3 stored ones): add half of the last kept place, ties
     // down when that place is even, and clear what is below
     float r = __uint_as_float((bits + 0x7ffffu + ((bits >> 20) & 1u)) & 0xfff00000u);
@@ -252,21 +254,48 @@ __device__ __forceinline__ int exponent_of(uint32_t amax_bits)
 // Magnitudes of two bf16 at or above this round up to infinity at 4 significant bits, or are not finite.
 constexpr uint32_t kHuge = 0x7f78u;
 
-// R(x * inv) of two bf16 values below kHuge, as two e4m3 bytes.  Rounding to 4 significant bits
-// works on the bf16 bits of both at once (dividing by a power of two changes no significant bit).
-// Cutting to a multiple of 2^-9 changes no value of 4 significant bits from 2^-6 on, so it needs no
-// case: with c = +-2^14, whose unit in the last place is 2^-9, (x inv + c, cut) - c is the cut.
-__device__ __forceinline__ uint32_t codes_of(uint32_t two, float inv)
+// The magnitude of f * |x| cut to a multiple of 2^-9: (|x| f + 2^14, cut) - 2^14, for 2^-9 is the
+// unit in the last place from 2^14 on.  Values of 4 significant bits from 2^-6 on are such multiples
+// and stay what they are, so the cut of R needs no case.
+__device__ __forceinline__ float cut(float x, float f) { return __fmaf_rz(fabsf(x), f, 16384.0f) - 16384.0f; }
+
+// Two non-negative values as e4m3 bytes: exact for values of R up to 448, saturating, NaN stays.
+__device__ __forceinline__ uint32_t bytes_of(float lo, float hi)
 {
-    const uint32_t r = (two + 0x00070007u + ((two >> 4) & 0x00010001u)) & 0xfff0fff0u;
-    const float lo = __uint_as_float(r << 16), hi = __uint_as_float(r & 0xffff0000u);
-    const float c_lo = copysignf(16384.0f, lo), c_hi = copysignf(16384.0f, hi);
-    // a value cut to zero keeps its sign, as in code_of
-    const float y_lo = copysignf(__fmaf_rz(lo, inv, c_lo) - c_lo, lo), y_hi = copysignf(__fmaf_rz(hi, inv, c_hi) - c_hi, hi);
     uint16_t y;
-    // exact for every value up to 448; saturates above
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(y) : "f"(y_hi), "f"(y_lo));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(y) : "f"(hi), "f"(lo));
     return y;
+}
+
+// R(x * inv) of four bf16 values below kHuge (two words), as four e4m3 bytes.  Rounding to 4
+// significant bits works on the bf16 bits of a pair at once (dividing by a power of two changes no
+// significant bit); the sign bits are the high bits of the bf16s' high bytes.
+__device__ __forceinline__ uint32_t codes_of(uint32_t a, uint32_t b, float inv)
+{
+    const uint32_t ra = (a + 0x00070007u + ((a >> 4) & 0x00010001u)) & 0xfff0fff0u;
+    const uint32_t rb = (b + 0x00070007u + ((b >> 4) & 0x00010001u)) & 0xfff0fff0u;
+    const uint32_t lo = bytes_of(cut(__uint_as_float(ra << 16), inv), cut(__uint_as_float(ra & 0xffff0000u), inv));
+    const uint32_t hi = bytes_of(cut(__uint_as_float(rb << 16), inv), cut(__uint_as_float(rb & 0xffff0000u), inv));
+    return __byte_perm(lo, hi, 0x5410) | (__byte_perm(a, b, 0x7531) & 0x80808080u);
+}
+
+// Four e4m3 codes moved to a scale 1 / f times theirs: R(code * f).
+__device__ __forceinline__ uint32_t moved(uint32_t codes, float f)
+{
+    uint32_t out[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        uint32_t h;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(codes >> (16 * j))));
+        const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+        out[j] = bytes_of(cut(v.x, f), cut(v.y, f));
+    }
+    const uint32_t r = __byte_perm(out[0], out[1], 0x5410);
+    // a NaN keeps no sign, as when it was written
+    uint32_t sign = codes & 0x80808080u;
+    if (__vcmpeq4(codes & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0)
+        sign &= ~__vcmpeq4(codes & 0x7f7f7f7fu, 0x7f7f7f7fu);
+    return r | sign;
 }
 
 // Largest of two bf16 magnitudes so far and in a word, packed.
@@ -287,8 +316,9 @@ __device__ __forceinline__ void group_sync(int group)
 }
 
 template <int D, int G>
-__global__ void __launch_bounds__(32 * kAppendWarps) kv_append_kernel(const __grid_constant__ AppendArgs a)
+__global__ void __launch_bounds__(32 * kAppendWarpsOf<G>) kv_append_kernel(const __grid_constant__ AppendArgs a)
 {
+    constexpr int kAppendWarps = kAppendWarpsOf<G>;
     constexpr int kVecs = D / 8;             // 16-byte vectors of a row's head
     constexpr int kTokens = 32 / kVecs;      // tokens one load instruction covers
     constexpr int kLoads = kPiece / kTokens;
@@ -377,18 +407,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) kv_append_kernel(const __gr
                 for (int y = begin * (D / 16) + lane; y < end * (D / 16); y += 32) {
                     uint4 *at = reinterpret_cast<uint4 *>(codes + (y / (D / 16)) * a.token_stride) + y % (D / 16);
                     uint4 q = *at;
-                    uint32_t *w = reinterpret_cast<uint32_t *>(&q);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t out = 0;
-#pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            __nv_fp8_e4m3 c;
-                            c.__x = static_cast<uint8_t>(w[j] >> (8 * b));
-                            out |= code_of(static_cast<float>(c) * f) << (8 * b);
-                        }
-                        w[j] = out;
-                    }
+                    q = make_uint4(moved(q.x, f), moved(q.y, f), moved(q.z, f), moved(q.w, f));
                     *at = q;
                 }
             } else {
@@ -403,20 +422,19 @@ __global__ void __launch_bounds__(32 * kAppendWarps) kv_append_kernel(const __gr
         for (int j = 0; j < kLoads; ++j) {
             const int tok = j * kTokens + lane / kVecs;
             if (tok < count) {
-                const uint32_t in[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-                uint32_t out[4];
+                uint2 out;
                 if (!huge) {
-#pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        out[y] = codes_of(in[y], inv);
+                    out = make_uint2(codes_of(v[j].x, v[j].y, inv), codes_of(v[j].z, v[j].w, inv));
                 } else {
+                    const uint32_t in[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+                    uint32_t two[4];
 #pragma unroll
                     for (int y = 0; y < 4; ++y)
-                        out[y] = code_of(__uint_as_float(in[y] << 16) * inv) |
+                        two[y] = code_of(__uint_as_float(in[y] << 16) * inv) |
                                  (code_of(__uint_as_float(in[y] & 0xffff0000u) * inv) << 8);
+                    out = make_uint2(two[0] | (two[1] << 16), two[2] | (two[3] << 16));
                 }
-                *reinterpret_cast<uint2 *>(to + tok * a.token_stride) =
-                    make_uint2(out[0] | (out[1] << 16), out[2] | (out[3] << 16));
+                *reinterpret_cast<uint2 *>(to + tok * a.token_stride) = out;
             }
         }
     }
@@ -425,8 +443,8 @@ __global__ void __launch_bounds__(32 * kAppendWarps) kv_append_kernel(const __gr
 template <int D, int G>
 bi_status_t run_append(const AppendArgs &a, int64_t blocks_of_rows, cudaStream_t stream)
 {
-    const int64_t units = blocks_of_rows * 2 * a.heads, per = kAppendWarps / G;
-    return bi_kv::launch(kv_append_kernel<D, G>, dim3(static_cast<unsigned>((units + per - 1) / per)), dim3(32 * kAppendWarps), 0,
+    const int64_t units = blocks_of_rows * 2 * a.heads, per = kAppendWarpsOf<G> / G;
+    return bi_kv::launch(kv_append_kernel<D, G>, dim3(static_cast<unsigned>((units + per - 1) / per)), dim3(32 * kAppendWarpsOf<G>), 0,
                          stream, 1, a);
 }
 

@@ -80,7 +80,7 @@ typedef struct {
  * free_left, status [1]; block_table [B][ld_table], ld_table >= max_pages; token_offsets [B + 1];
  * slot_map, positions [max_tokens] (positions may be NULL).  seq_lens may be ctx_lens and
  * free_left may be free_count (a captured step that is replayed); other arrays must not overlap.
- * Limits: 0 <= B <= 8192, max_pages * page_size < 2^31, max_tokens < 2^31.
+ * Limits: 0 <= B <= 8192, max_pages * page_size < 2^31, max_tokens and free_capacity <= 2^30.
  * Errors: BI_ERR_INVALID_ARG, BI_ERR_ALIGNMENT (4 bytes), BI_ERR_UNSUPPORTED_SHAPE,
  * BI_ERR_NO_DEVICE, BI_ERR_CUDA.
  */

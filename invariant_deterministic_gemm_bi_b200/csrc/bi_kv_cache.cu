@@ -15,16 +15,18 @@ namespace {
 using bi_kv::kFull;
 
 // ---------------------------------------------------------------------------------------------
-// Block tables and slot maps.  One cluster; every CTA reads all lengths and scans them by itself
-// (new tokens, new pages, returned pages), so the CTAs share no partial sums, and after one
-// cluster barrier -- every input that an output may alias has been read -- each writes its share.
-// Latency bound: a few hundred KB at most.  Threads find the request of their token or page by a
-// binary search in the scanned sums, which sit in shared memory.
+// Block tables and slot maps.  One cluster of one to eight CTAs; every CTA reads all lengths and
+// scans them by itself (new tokens, new pages, returned pages), so the CTAs share no partial sums,
+// and after one cluster barrier -- every input that an output may alias has been read -- each writes
+// its share.  Latency bound: a few hundred KB at most.  Threads find the request of their token or
+// page by a binary search in the scanned sums, which sit in shared memory, once for four consecutive
+// tokens.  (A search for every token kept eight SMs busy for 9 us over 51k tokens.)
 // ---------------------------------------------------------------------------------------------
 
 constexpr int kTableThreads = 1024;
-constexpr int kTableCluster = 8;
+constexpr int kTableTokens = 4;      // consecutive tokens of a thread
 constexpr int kMaxRequests = 8192;   // four int32 arrays of it in shared memory: 128 KB
+constexpr int32_t kMostItems = 1 << 30;   // tokens of a call, pages on the stack
 
 struct TableArgs {
     const int32_t *ctx_lens, *new_lens, *free_count;
@@ -33,15 +35,46 @@ struct TableArgs {
     int b, page_shift;
 };
 
+// Sums that stop at 2^31 - 1 (no valid call reaches it), so that no lengths make them wrap.
 struct Sums {
-    int64_t tokens, need, back;
+    uint32_t tokens, need, back;
 };
 
-__device__ __forceinline__ Sums operator+(Sums a, Sums b) { return {a.tokens + b.tokens, a.need + b.need, a.back + b.back}; }
+__device__ __forceinline__ uint32_t capped(uint32_t a, uint32_t b) { return min(a + b, 0x7fffffffu); }
+__device__ __forceinline__ Sums operator+(Sums a, Sums b)
+{
+    return {capped(a.tokens, b.tokens), capped(a.need, b.need), capped(a.back, b.back)};
+}
 
 __device__ __forceinline__ Sums shfl_up(Sums s, int off)
 {
     return {__shfl_up_sync(kFull, s.tokens, off), __shfl_up_sync(kFull, s.need, off), __shfl_up_sync(kFull, s.back, off)};
+}
+__device__ __forceinline__ Sums shfl(Sums s, int from)
+{
+    return {__shfl_sync(kFull, s.tokens, from), __shfl_sync(kFull, s.need, from), __shfl_sync(kFull, s.back, from)};
+}
+__device__ __forceinline__ Sums warp_scan(Sums s)   // inclusive
+{
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const Sums y = shfl_up(s, off);
+        if ((threadIdx.x & 31) >= off)
+            s = s + y;
+    }
+    return s;
+}
+
+// What request i adds: ctx tokens in the cache, `add` new ones, 2^shift tokens a page.
+__device__ __forceinline__ Sums request(int64_t ctx, int64_t add, int shift, int64_t max_pages)
+{
+    const int64_t page = INT64_C(1) << shift;
+    const int64_t have = (ctx + page - 1) >> shift, end = (ctx + (add > 0 ? add : 0) + page - 1) >> shift;
+    Sums s = {static_cast<uint32_t>(add > 0 ? add : 0), static_cast<uint32_t>(add >= 0 ? end - have : 0),
+              static_cast<uint32_t>(add < 0 ? have : 0)};
+    if (end > max_pages)   // does not fit: more tokens than any call may have
+        s.tokens = 0x7fffffffu;
+    return s;
 }
 
 // The last i in [0, n) with sums[i] <= x, for ascending sums with sums[0] = 0 <= x < sums[n]: the
@@ -80,60 +113,43 @@ __global__ void __launch_bounds__(kTableThreads, 1) kv_tables_kernel(TableArgs a
     const int per = (a.b + kTableThreads - 1) / kTableThreads;
     const int lo = min(tid * per, a.b), hi = min(lo + per, a.b);
     Sums mine = {0, 0, 0};
-    bool bad = false, wide = false;
+    bool bad = false;
     for (int i = lo; i < hi; ++i) {
-        const int64_t ctx = a.ctx_lens[i], add = a.new_lens[i];
+        const int ctx = a.ctx_lens[i], add = a.new_lens[i];
         bad |= ctx < 0 || add < -1;
-        const int64_t have = (ctx + page - 1) >> a.page_shift;
-        const int64_t end = (ctx + (add > 0 ? add : 0) + page - 1) >> a.page_shift;
-        wide |= end > a.max_pages;
-        ctx_s[i] = static_cast<int32_t>(ctx);
-        mine = mine + Sums{add > 0 ? add : 0, add >= 0 ? end - have : 0, add < 0 ? have : 0};
+        ctx_s[i] = ctx;
+        tok_s[i] = add;   // the sums take its place below
+        mine = mine + request(ctx, add, a.page_shift, a.max_pages);
     }
-    Sums incl = mine;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const Sums y = shfl_up(incl, off);
-        if (lane >= off)
-            incl = incl + y;
-    }
+    const int64_t count = *a.free_count;
+    const Sums incl = warp_scan(mine);
     if (lane == 31)
         warp_sums[warp] = incl;
     const bool any_bad = __syncthreads_or(bad);
-    const bool any_wide = __syncthreads_or(wide);
-    Sums before = {0, 0, 0}, total = {0, 0, 0};
-    for (int w = 0; w < kTableThreads / 32; ++w) {
-        if (w == warp)
-            before = total;
-        total = total + warp_sums[w];
-    }
-    const int64_t count = *a.free_count;
+    const Sums warps = warp_scan(warp_sums[lane]), total = shfl(warps, 31);
+    const Sums before = shfl(warps, max(warp - 1, 0));
     int status = BI_OK;
     if (any_bad || count < 0 || count > a.free_capacity)
         status = BI_ERR_INVALID_ARG;
-    else if (any_wide || total.tokens > a.max_tokens || count + total.back > a.free_capacity ||
-             total.need > count + total.back)
+    else if (total.tokens > a.max_tokens || count + total.back > a.free_capacity || total.need > count + total.back)
         status = BI_ERR_UNSUPPORTED_SHAPE;
-    if (status == BI_OK) {   // every sum is below 2^31
-        Sums run = {before.tokens + incl.tokens - mine.tokens, before.need + incl.need - mine.need,
-                    before.back + incl.back - mine.back};
+    if (status == BI_OK) {   // no sum has reached its cap
+        Sums run = {incl.tokens - mine.tokens, incl.need - mine.need, incl.back - mine.back};
+        if (warp > 0)
+            run = run + before;
         for (int i = lo; i < hi; ++i) {
-            const int64_t ctx = ctx_s[i], add = a.new_lens[i];
-            const int64_t have = (ctx + page - 1) >> a.page_shift;
-            tok_s[i] = static_cast<int32_t>(run.tokens);
-            need_s[i] = static_cast<int32_t>(run.need);
-            back_s[i] = static_cast<int32_t>(run.back);
-            run.tokens += add > 0 ? add : 0;
-            run.need += add >= 0 ? ((ctx + add + page - 1) >> a.page_shift) - have : 0;
-            run.back += add < 0 ? have : 0;
+            const Sums r = request(ctx_s[i], tok_s[i], a.page_shift, a.max_pages);
+            tok_s[i] = run.tokens;
+            need_s[i] = run.need;
+            back_s[i] = run.back;
+            run = run + r;
         }
         if (tid == 0) {
-            tok_s[a.b] = static_cast<int32_t>(total.tokens);
-            need_s[a.b] = static_cast<int32_t>(total.need);
-            back_s[a.b] = static_cast<int32_t>(total.back);
+            tok_s[a.b] = total.tokens;
+            need_s[a.b] = total.need;
+            back_s[a.b] = total.back;
         }
     }
-    // whether request i has ended, before seq_lens (which may be ctx_lens) is written
     const int64_t gid = static_cast<int64_t>(blockIdx.x) * kTableThreads + tid;
     const int64_t gsize = static_cast<int64_t>(gridDim.x) * kTableThreads;
     cluster_barrier();   // every CTA's shared memory is ready, and every CTA has read the lengths
@@ -171,23 +187,42 @@ __global__ void __launch_bounds__(kTableThreads, 1) kv_tables_kernel(TableArgs a
         const int64_t have = (static_cast<int64_t>(ctx_s[i]) + page - 1) >> a.page_shift;
         a.block_table[i * a.ld_table + have + (r - need_s[i])] = __ldcg(a.free_pages + (top - 1 - r));
     }
-    for (int64_t t = gid; t < a.max_tokens; t += gsize) {
-        int64_t slot = -1, pos = -1;
-        if (t < tokens) {
-            const int i = owner(tok_s, a.b, static_cast<int32_t>(t));
-            pos = static_cast<int64_t>(ctx_s[i]) + (t - tok_s[i]);
-            const int64_t p = pos >> a.page_shift;
-            const int64_t have = (static_cast<int64_t>(ctx_s[i]) + page - 1) >> a.page_shift;
-            // a page of this call is read from the stack, not from the entry another CTA may still write
-            const int64_t id = p < have ? a.block_table[i * a.ld_table + p]
-                                        : __ldcg(a.free_pages + (top - 1 - (need_s[i] + (p - have))));
-            slot = (id << a.page_shift) + (pos & (page - 1));
-            if (id < 0 || slot > INT32_MAX)
-                slot = -1;
+    const bool vec = ((reinterpret_cast<uintptr_t>(a.slot_map) | reinterpret_cast<uintptr_t>(a.positions)) & 15u) == 0;
+    for (int64_t t0 = kTableTokens * gid; t0 < a.max_tokens; t0 += kTableTokens * gsize) {
+        int32_t pos[kTableTokens], id[kTableTokens], slots[kTableTokens];
+        int i = t0 < tokens ? owner(tok_s, a.b, static_cast<int32_t>(t0)) : 0;
+#pragma unroll
+        for (int j = 0; j < kTableTokens; ++j) {
+            const int64_t t = t0 + j;
+            pos[j] = -1;
+            id[j] = -1;
+            if (t < tokens) {
+                while (tok_s[i + 1] <= t)   // t < tok_s[b]: ends
+                    ++i;
+                pos[j] = ctx_s[i] + static_cast<int32_t>(t - tok_s[i]);   // below max_pages * page
+                const int32_t p = pos[j] >> a.page_shift;
+                const int32_t have = static_cast<int32_t>((static_cast<int64_t>(ctx_s[i]) + page - 1) >> a.page_shift);
+                // a page of this call is read from the stack, not from the entry another CTA may still write
+                const int32_t *from = p < have ? a.block_table + i * a.ld_table + p : a.free_pages + (top - 1 - (need_s[i] + (p - have)));
+                id[j] = __ldcg(from);
+            }
         }
-        a.slot_map[t] = static_cast<int32_t>(slot);
-        if (a.positions)
-            a.positions[t] = static_cast<int32_t>(pos);
+#pragma unroll
+        for (int j = 0; j < kTableTokens; ++j) {
+            const int64_t slot = (static_cast<int64_t>(id[j]) << a.page_shift) + (pos[j] & (page - 1));
+            slots[j] = id[j] < 0 || slot > INT32_MAX ? -1 : static_cast<int32_t>(slot);
+        }
+        if (vec && t0 + kTableTokens <= a.max_tokens) {
+            *reinterpret_cast<int4 *>(a.slot_map + t0) = make_int4(slots[0], slots[1], slots[2], slots[3]);
+            if (a.positions)
+                *reinterpret_cast<int4 *>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        } else {
+            for (int j = 0; j < kTableTokens && t0 + j < a.max_tokens; ++j) {
+                a.slot_map[t0 + j] = slots[j];
+                if (a.positions)
+                    a.positions[t0 + j] = pos[j];
+            }
+        }
     }
     for (int64_t i = gid; i <= a.b; i += gsize) {
         a.token_offsets[i] = tok_s[i];
@@ -615,7 +650,7 @@ bi_status_t bi_kv_block_tables(const int32_t *ctx_lens, const int32_t *new_lens,
     if (B < 0 || free_capacity < 0 || max_pages < 0 || ld_table < max_pages || max_tokens < 0)
         return BI_ERR_INVALID_ARG;
     if (!bi_kv::valid_page_size(page_size) || B > kMaxRequests || max_pages > INT32_MAX / page_size ||
-        max_tokens > INT32_MAX || free_capacity > INT32_MAX || ld_table > (INT64_C(1) << 40))
+        max_tokens > kMostItems || free_capacity > kMostItems || ld_table > (INT64_C(1) << 40))
         return BI_ERR_UNSUPPORTED_SHAPE;
     if (!free_count || !free_left || !status || !token_offsets || (B > 0 && (!ctx_lens || !new_lens || !seq_lens)) ||
         (B > 0 && max_pages > 0 && !block_table) || (free_capacity > 0 && !free_pages) || (max_tokens > 0 && !slot_map))
@@ -656,7 +691,11 @@ bi_status_t bi_kv_block_tables(const int32_t *ctx_lens, const int32_t *new_lens,
         cudaGetLastError();
         return BI_ERR_CUDA;
     }
-    return bi_kv::launch(kv_tables_kernel, dim3(kTableCluster), dim3(kTableThreads), smem, stream, kTableCluster, a);
+    // CTAs: one for every 4096 tokens, up to a portable cluster
+    int cluster = 1;
+    while (cluster < 8 && static_cast<int64_t>(cluster) * kTableThreads * kTableTokens < (max_tokens > B ? max_tokens : B))
+        cluster *= 2;
+    return bi_kv::launch(kv_tables_kernel, dim3(cluster), dim3(kTableThreads), smem, stream, cluster, a);
 }
 
 bi_status_t bi_kv_append_e4m3(const bi_kv_cache_t *cache, const void *K, int64_t ldk, const void *V,

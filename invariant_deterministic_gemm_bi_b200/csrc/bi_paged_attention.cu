@@ -6,7 +6,7 @@
 //
 // Work.  A sequence's positions are cut into steps of 256 at multiples of 256, and runs of steps
 // into chunks whose length follows from the number of steps alone.  An item is one chunk of one
-// key/value head; persistent CTAs take items round robin, those of long chunks first so that short
+// key/value head; persistent CTAs take items round robin, those of most steps first so that short
 // ones fill the gaps at the end.  Consumer warp w of a CTA owns positions
 // 32 w .. 32 w + 31 of every step and keeps a softmax state of its own over the chunk; the eight
 // states are added in warp order at the chunk's end, and the chunks in ascending order by a second
@@ -62,11 +62,11 @@ constexpr int kHalf = kTiles * kTile;       // positions of a stage: half a step
 constexpr int kStep = kConsumers * kTile;   // positions of a CTA's step
 constexpr int kMaxChunks = 128;             // chunks of a sequence
 constexpr int kMaxGroup = 16;               // query heads of a key/value head
-constexpr int kEntries = 512;               // entries of the scanned chunk counts
-constexpr int kClasses = 3;                 // of sequences, by steps per chunk: 4 and more, 2, 1
+constexpr int kEntries = 256;               // entries of the scanned chunk counts
+constexpr int kClasses = 4;                 // of chunks, by steps: 4 and more, 3, 2, 1
 constexpr int kItemBlock = 32;              // items whose table entries one warp makes at once
 constexpr int kItemRing = 4 * kItemBlock;   // entries of the items' table
-constexpr int kMaxBatch = kEntries * 32;    // an entry stands for up to 32 sequences
+constexpr int kMaxBatch = 16384;            // sequences; an entry stands for several when there are more than entries
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kWeightExp = 15.0f;         // weights are held times 2^15
@@ -105,7 +105,7 @@ struct Span {
     bool bad;
 };
 
-__host__ __device__ __forceinline__ int class_of(int per_chunk) { return per_chunk >= 4 ? 0 : per_chunk == 2 ? 1 : 2; }
+__host__ __device__ __forceinline__ int class_of(int steps) { return steps >= 4 ? 0 : 4 - steps; }
 
 __device__ __forceinline__ Span span_of(int len, const AttnArgs &a)
 {
@@ -119,6 +119,13 @@ __device__ __forceinline__ Span span_of(int len, const AttnArgs &a)
     s.per_chunk = chunk_steps(s.steps);
     s.chunks = (s.steps + s.per_chunk - 1) / s.per_chunk;
     return s;
+}
+
+// How many chunks of class c a span has: its whole chunks, and a shorter last one.
+__device__ __forceinline__ int chunks_of_class(const Span &s, int c)
+{
+    const int whole = s.steps / s.per_chunk, rest = s.steps - whole * s.per_chunk;
+    return (class_of(s.per_chunk) == c ? whole : 0) + (rest > 0 && class_of(rest) == c ? 1 : 0);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -287,7 +294,10 @@ __device__ __forceinline__ Item make_item(const AttnArgs &a, const S &sm, int i)
     Item it = {};
     const int64_t n = blockIdx.x + static_cast<int64_t>(i) * gridDim.x;
     it.b = -1;
-    const int most = sm.class_chunks[0] + sm.class_chunks[1] + sm.class_chunks[2];
+    int most = 0;
+#pragma unroll
+    for (int c = 0; c < kClasses; ++c)
+        most += sm.class_chunks[c];
     if (n >= static_cast<int64_t>(most) * a.heads)
         return it;
     int chunk = static_cast<int>(n) / a.heads;
@@ -306,11 +316,15 @@ __device__ __forceinline__ Item make_item(const AttnArgs &a, const S &sm, int i)
     Span s;
     if (a.b <= kEntries) {
         s = span_of(sm.len[b], a);
-    } else {   // an entry is several consecutive sequences, of which those of the class count
+    } else {   // an entry is several consecutive sequences
         b = e * ((a.b + kEntries - 1) / kEntries);
-        for (s = span_of(a.lens[b], a); class_of(s.per_chunk) != cls || chunk >= s.chunks; s = span_of(a.lens[++b], a))
-            chunk -= class_of(s.per_chunk) == cls ? s.chunks : 0;
+        s = span_of(a.lens[b], a);
+        for (int n_here; chunk >= (n_here = chunks_of_class(s, cls)); s = span_of(a.lens[++b], a))
+            chunk -= n_here;
     }
+    // of a sequence's chunks of the class: the whole ones from the first on, or its last
+    if (class_of(s.per_chunk) != cls)
+        chunk = s.chunks - 1;
     it.b = b;
     it.lo = s.lo;
     it.hi = s.hi;
@@ -759,27 +773,23 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_c
         (&sm.qc[0][0])[tid] = 0.0f;
     bi_kv::dependency_wait();
 
-    // chunks before each entry, class by class: thread i scans entries 2 i and 2 i + 1
+    // chunks before each entry, class by class, one entry a thread
     const int per = (a.b + kEntries - 1) / kEntries;
-    static_assert(2 * kThreads >= kEntries, "two entries a thread");
-    int n[2][kClasses] = {}, incl[kClasses];
+    static_assert(kThreads >= kEntries, "one entry a thread");
+    int n[kClasses] = {}, incl[kClasses];
+    if (tid < kEntries)
+        for (int b = tid * per; b < (tid + 1) * per && b < a.b; ++b) {
+            const int len = a.lens[b];
+            if (per == 1)
+                sm.len[tid] = len;
+            const Span s = span_of(len, a);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int e = 2 * tid + j;
-        if (e < kEntries)
-            for (int b = e * per; b < (e + 1) * per && b < a.b; ++b) {
-                const int len = a.lens[b];
-                if (per == 1)
-                    sm.len[e] = len;
-                const Span s = span_of(len, a);
-#pragma unroll
-                for (int c = 0; c < kClasses; ++c)
-                    n[j][c] += class_of(s.per_chunk) == c ? s.chunks : 0;
-            }
-    }
+            for (int c = 0; c < kClasses; ++c)
+                n[c] += chunks_of_class(s, c);
+        }
 #pragma unroll
     for (int c = 0; c < kClasses; ++c) {
-        incl[c] = n[0][c] + n[1][c];
+        incl[c] = n[c];
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int y = __shfl_up_sync(kFull, incl[c], off);
@@ -792,18 +802,15 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_c
     __syncthreads();
 #pragma unroll
     for (int c = 0; c < kClasses; ++c) {
-        int before = incl[c] - n[0][c] - n[1][c], total = 0;
+        int before = incl[c] - n[c], total = 0;
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) {
+        for (int w = 0; w < kEntries / 32; ++w) {
             before += w < warp ? sm.warp_sum[c][w] : 0;
             total += sm.warp_sum[c][w];
         }
         // entries behind the last sequence hold INT_MAX
-        const int used = (a.b + per - 1) / per;
-        if (2 * tid < kEntries) {
-            sm.first_chunk[c][2 * tid] = 2 * tid < used ? before : INT_MAX;
-            sm.first_chunk[c][2 * tid + 1] = 2 * tid + 1 < used ? before + n[0][c] : INT_MAX;
-        }
+        if (tid < kEntries)
+            sm.first_chunk[c][tid] = tid * per < a.b ? before : INT_MAX;
         if (tid == 0)
             sm.class_chunks[c] = total;
     }

@@ -230,24 +230,27 @@ template <int D, int MG>
 struct Shared {
     static constexpr int NT = MG > 8 ? 2 : 1;
     static constexpr int kCols = NT * 8;
-    // 32 KB stages of D = 128 (16 KB of D = 64) beside the chunk states, 208 KB together at most.  A
-    // stage always serves the same half of the steps: a consumer then waits for every use of its
-    // stages in turn, which waiting by parity needs.
-    static constexpr int kStages = D == 128 ? (MG == 4 ? 6 : 4) : 10;
+    // 32 KB stages of D = 128 (16 KB of D = 64) beside the chunk states, 192 KB together.  A stage always
+    // serves the same half of the steps: a consumer then waits for every use of its stages in turn,
+    // which waiting by parity needs.
+    static constexpr int kStages = D == 128 ? 4 : MG > 8 ? 8 : 10;
+    // States of two chunks, so that one is added while the next is written (16 heads of 128: one).
+    static constexpr int kStates = D * MG > 1024 ? 1 : 2;
     static_assert(kStages % 2 == 0, "two halves");
     static constexpr int kMatrix = kTile * D;               // bytes of a tile's keys (or values)
     uint8_t ring[kStages][kTiles][2][kMatrix];              // keys, values
-    float state[kConsumers][MG][D];                         // a chunk's outputs, not normalised
+    float state[kStates][kConsumers][MG][D];                // a chunk's outputs, not normalised
     uint4 q[2][NT][D / 32][32];                             // two items' queries, as the consumers' lanes hold them
     float4 scale[kStages][kHalf / 16];                      // of 16 positions: key scale, log2 and 1 / of the value scale
     Item items[kItemRing];
     Stage stage[kStages];
-    float2 ml[kConsumers][kCols];                           // a chunk's maxima and sums
+    float2 ml[kStates][kConsumers][kCols];                  // a chunk's maxima and sums
     float qc[2][kCols];                                     // scale * log2 e * the power of two taken out
     uint64_t full[kStages], empty[kStages];                 // a stage is filled, is consumed
-    // A chunk's states are written; the helpers have read the states of the item before and prepared
-    // the queries of the one after (even and odd items apart: the helpers may be one ahead).
-    uint64_t states, helped[2];
+    // An item's states are written; the helpers are done with the item two before: its states are read,
+    // and the queries that take the place of its own are there.  Even and odd items apart, since
+    // consumers and helpers may be one ahead.
+    uint64_t states[2], helped[2];
     int32_t first_chunk[kClasses][kEntries];                // chunks of the class before each entry
     int32_t class_chunks[kClasses];
     int32_t len[kEntries];                                  // lengths, when an entry is one sequence
@@ -459,13 +462,13 @@ __device__ __forceinline__ void consume(Shared<D, MG> &sm, const AttnArgs &a, in
     int slot = warp / kTiles;         // stages of this warp's half of the steps
     uint32_t parity = 0;
     int item = 0;
-    wait_for(sm, &sm.helped[0], 0);
     while (true) {
         wait_for(sm, &sm.full[slot], parity);
         const Stage st = sm.stage[slot];
         if ((st.flags & kEnd) || *static_cast<volatile int *>(&sm.dead))
             break;
         if (st.flags & kFirst) {
+            wait_for(sm, &sm.helped[item & 1], (item >> 1) & 1);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -617,8 +620,10 @@ __device__ __forceinline__ void consume(Shared<D, MG> &sm, const AttnArgs &a, in
             parity ^= 1;
         }
         if (st.flags & kLast) {
+            const int buf = S::kStates == 1 ? 0 : item & 1;
             ++item;
-            wait_for(sm, &sm.helped[item & 1], (item >> 1) & 1);   // the states of the item before have been read
+            if constexpr (S::kStates == 1)
+                wait_for(sm, &sm.helped[item & 1], (item >> 1) & 1);   // the states of the item before have been read
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -629,64 +634,89 @@ __device__ __forceinline__ void consume(Shared<D, MG> &sm, const AttnArgs &a, in
                     x += __shfl_xor_sync(kFull, x, 16);
                     const int head = n * 8 + 2 * t + h;
                     if (g == 0)
-                        sm.ml[warp][head] = make_float2(m[n][h], x);
+                        sm.ml[buf][warp][head] = make_float2(m[n][h], x);
                     if (head < a.group) {
 #pragma unroll
                         for (int j = 0; j < D / 16; ++j)
-                            *reinterpret_cast<float2 *>(&sm.state[warp][0][0] + state_offset<D>(head, 16 * j + 2 * g)) =
+                            *reinterpret_cast<float2 *>(&sm.state[buf][warp][0][0] + state_offset<D>(head, 16 * j + 2 * g)) =
                                 make_float2(o[n][j][h], o[n][j][2 + h]);
                     }
                 }
-            warp_arrive(&sm.states);
+            warp_arrive(&sm.states[(item - 1) & 1]);
         }
     }
 }
 
-// Queries of an item, as the consumers' lanes hold them: helper warp w converts heads w, w + 4, ...
+// Queries of an item as fp16 with a power of two taken out: helper warp w converts heads w, w +
+// kHelpers, ..., four dimensions a lane.
 template <int D, int MG>
-__device__ __forceinline__ void prepare_queries(Shared<D, MG> &sm, const AttnArgs &a, const Item &it, int buf, int w)
-{
-    const int lane = threadIdx.x & 31;
-    for (int head = w; head < a.group; head += kHelpers) {
-        uint2 raw = make_uint2(0, 0);
-        if (lane < D / 4)   // four dimensions a lane
-            raw = *(reinterpret_cast<const uint2 *>(a.q + it.b * a.ldq + static_cast<int64_t>(it.kvh * a.group + head) * D) + lane);
-        uint32_t top = max(max(raw.x & 0x7fffu, (raw.x >> 16) & 0x7fffu), max(raw.y & 0x7fffu, (raw.y >> 16) & 0x7fffu));
-        top = __reduce_max_sync(kFull, top);
-        // the largest magnitude goes to [2^14, 2^15)
-        const int e = top == 0 ? 0 : max(-120, static_cast<int>(top >> 7) - 127 - 14);
-        const float down = pow2(-e);
-        if (lane < D / 4) {
-            uint2 x;
-            x.x = pack_half(__uint_as_float(raw.x << 16) * down, __uint_as_float(raw.x & 0xffff0000u) * down);
-            x.y = pack_half(__uint_as_float(raw.y << 16) * down, __uint_as_float(raw.y & 0xffff0000u) * down);
-            const int ks = lane >> 2;
-            reinterpret_cast<uint2 *>(&sm.q[buf][head >> 3][ks >> 1][(head & 7) * 4 + (lane & 3)])[ks & 1] = x;
+struct Queries {
+    static constexpr int kHeads = (MG + kHelpers - 1) / kHelpers;
+    uint2 x[kHeads];
+    float c[kHeads];
+
+    __device__ __forceinline__ void load(const AttnArgs &a, const Item &it, int w)
+    {
+        const int lane = threadIdx.x & 31;
+        const __nv_bfloat16 *from = a.q + it.b * a.ldq + static_cast<int64_t>(it.kvh) * a.group * D + lane * 4;
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i) {
+            const int head = w + i * kHelpers;
+            x[i] = make_uint2(0, 0);
+            if (it.b >= 0 && head < a.group && lane < D / 4)
+                x[i] = __ldg(reinterpret_cast<const uint2 *>(from + head * D));
         }
-        if (lane == 0)
-            sm.qc[buf][head] = a.scale * kLog2e * pow2(e);
     }
-}
+    __device__ __forceinline__ void convert(const AttnArgs &a)
+    {
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i) {
+            uint32_t top = max(max(x[i].x & 0x7fffu, (x[i].x >> 16) & 0x7fffu), max(x[i].y & 0x7fffu, (x[i].y >> 16) & 0x7fffu));
+            top = __reduce_max_sync(kFull, top);
+            // the largest magnitude goes to [2^14, 2^15)
+            const int e = top == 0 ? 0 : max(-120, static_cast<int>(top >> 7) - 127 - 14);
+            const float down = pow2(-e);
+            x[i] = make_uint2(pack_half(__uint_as_float(x[i].x << 16) * down, __uint_as_float(x[i].x & 0xffff0000u) * down),
+                              pack_half(__uint_as_float(x[i].y << 16) * down, __uint_as_float(x[i].y & 0xffff0000u) * down));
+            c[i] = a.scale * kLog2e * pow2(e);
+        }
+    }
+    __device__ __forceinline__ void store(Shared<D, MG> &sm, const AttnArgs &a, int buf, int w) const
+    {
+        const int lane = threadIdx.x & 31, ks = lane >> 2;
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i) {
+            const int head = w + i * kHelpers;
+            if (head < a.group) {
+                if (lane < D / 4)   // as the consumers' lanes hold them
+                    reinterpret_cast<uint2 *>(&sm.q[buf][head >> 3][ks >> 1][(head & 7) * 4 + (lane & 3)])[ks & 1] = x[i];
+                if (lane == 0)
+                    sm.qc[buf][head] = c[i];
+            }
+        }
+    }
+};
 
 // The eight states of an item added in warp order, and the result or the chunk's part stored.
 template <int D, int MG>
-__device__ __forceinline__ void add_states(Shared<D, MG> &sm, const AttnArgs &a, const Item &it, int tid)
+__device__ __forceinline__ void add_states(Shared<D, MG> &sm, const AttnArgs &a, const Item &it, int buf, int tid)
 {
     constexpr int kQuads = D / 4;
+#pragma unroll 2
     for (int x = tid; x < a.group * kQuads; x += 32 * kHelpers) {
         const int head = x / kQuads, dd = (x % kQuads) * 4;
         float2 ml[kConsumers];
         float mx = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kConsumers; ++w) {
-            ml[w] = sm.ml[w][head];
+            ml[w] = sm.ml[buf][w][head];
             mx = fmaxf(mx, ml[w].x);
         }
         float sum = 0.0f;
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int w = 0; w < kConsumers; ++w) {
-            const float4 v = *reinterpret_cast<const float4 *>(&sm.state[w][0][0] + state_offset<D>(head, dd));
+            const float4 v = *reinterpret_cast<const float4 *>(&sm.state[buf][w][0][0] + state_offset<D>(head, dd));
             const float f = exp2_approx(ml[w].x - mx);
             sum = fmaf(ml[w].y, f, sum);
             acc.x = fmaf(v.x, f, acc.x);
@@ -719,26 +749,31 @@ __device__ __forceinline__ void add_states(Shared<D, MG> &sm, const AttnArgs &a,
 template <int D, int MG>
 __device__ __forceinline__ void help(Shared<D, MG> &sm, const AttnArgs &a, int w)
 {
+    Queries<D, MG> q;
     for (int i = 0; i < 2; ++i) {
-        const Item it = sm.items[i];
-        if (it.b >= 0)
-            prepare_queries(sm, a, it, i, w);
+        q.load(a, sm.items[i], w);
+        q.convert(a);
+        q.store(sm, a, i, w);
         warp_arrive(&sm.helped[i]);
     }
     for (int i = 0;; ++i) {
         const Item now = sm.items[i % kItemRing];
         if (now.b < 0)
             break;
-        wait_for(sm, &sm.states, i & 1);
-        add_states(sm, a, now, threadIdx.x - 32 * kConsumers);
+        // the queries of the item after next come while this one's states do (both in turn took 1.3 us
+        // an item, more than a chunk of one step)
         const Item then = sm.items[(i + 2) % kItemRing];
+        q.load(a, then, w);
+        q.convert(a);
+        wait_for(sm, &sm.states[i & 1], (i >> 1) & 1);
         if (then.b >= 0)
-            prepare_queries(sm, a, then, i & 1, w);
-        // The block of the table before item i's makes room for the one four further on: no helper
-        // warp is behind item i (its states were written after all of them had arrived for the item
-        // before), and the other warps read the new entries behind the barriers of the items between.
-        if (w == 0 && i > 0 && i % kItemBlock == 0) {
-            const int lane = threadIdx.x & 31, first = i - kItemBlock;
+            q.store(sm, a, i & 1, w);   // every consumer has read item i's
+        add_states(sm, a, now, Shared<D, MG>::kStates == 1 ? 0 : i & 1, threadIdx.x - 32 * kConsumers);
+        // A block of the table whose items are behind item i - 1 makes room for the one four further on.
+        // No helper warp is behind item i - 1 (item i's states were written after all of them had arrived
+        // for item i - 2), and the other warps read the new entries behind the barriers of the items between.
+        if (w == 0 && i > 1 && (i - 1) % kItemBlock == 0) {
+            const int lane = threadIdx.x & 31, first = i - 1 - kItemBlock;
             sm.items[(first + lane) % kItemRing] = make_item(a, sm, first + kItemRing + lane);
         }
         warp_arrive(&sm.helped[i & 1]);
@@ -758,7 +793,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_c
             bi::ptx::mbar_init(&sm.full[i], 1);
             bi::ptx::mbar_init(&sm.empty[i], kTiles);
         }
-        bi::ptx::mbar_init(&sm.states, kConsumers);
+        bi::ptx::mbar_init(&sm.states[0], kConsumers);
+        bi::ptx::mbar_init(&sm.states[1], kConsumers);
         bi::ptx::mbar_init(&sm.helped[0], kHelpers);
         bi::ptx::mbar_init(&sm.helped[1], kHelpers);
         bi::ptx::fence_mbarrier_init();

@@ -505,14 +505,14 @@ def bi_quantize_e2m1(W, w_scale, Q, w_zero=None, stream=None):
 # A decode step makes these calls once a layer, so their checks are kept short: shapes and strides
 # are read once, and tensors of one kind go through one loop.
 
-def _require(device, dtype, **tensors):
+def _require(device, dtype, names, *tensors):
     """Every tensor (None is passed over) on the current device, contiguous and of the given type."""
-    for name, t in tensors.items():
-        if t is not None:
-            if t.dtype is not dtype or not t.is_contiguous():
-                raise TypeError(f"{name} must be a contiguous {dtype} tensor")
+    for t in tensors:
+        if t is not None and (t.dtype is not dtype or not t.is_contiguous() or t.get_device() != device):
+            name = names.split()[[x is t for x in tensors].index(True)]
             if t.get_device() != device:
                 raise ValueError(f"{name} must be on the current device cuda:{device}")
+            raise TypeError(f"{name} must be a contiguous {dtype} tensor")
 
 
 def _current_device() -> int:
@@ -595,9 +595,9 @@ def bi_kv_block_tables(ctx_lens, new_lens, page_size: int, free_pages, free_coun
     free_left, status [1].  seq_lens may be ctx_lens and free_left may be free_count."""
     import torch
     device = _current_device()
-    _require(device, torch.int32, ctx_lens=ctx_lens, new_lens=new_lens, free_pages=free_pages,
-             free_count=free_count, seq_lens=seq_lens, token_offsets=token_offsets, slot_map=slot_map,
-             free_left=free_left, status=status, positions=positions)
+    _require(device, torch.int32, "ctx_lens new_lens free_pages free_count seq_lens token_offsets slot_map "
+             "free_left status positions", ctx_lens, new_lens, free_pages, free_count, seq_lens, token_offsets,
+             slot_map, free_left, status, positions)
     B, tokens = ctx_lens.numel(), slot_map.numel()
     rows, width, ld = _block_table(block_table, device)
     if rows != B or new_lens.numel() != B or seq_lens.numel() != B or token_offsets.numel() != B + 1 or \
@@ -617,7 +617,7 @@ def bi_kv_append_e4m3(cache: KvCache, K, V, slot_map, stream=None):
     device = _current_device()
     T, ldk = _heads_rows("K", K, device, cache.num_heads, cache.head_dim)
     rows, ldv = _heads_rows("V", V, device, cache.num_heads, cache.head_dim)
-    _require(device, torch.int32, slot_map=slot_map)
+    _require(device, torch.int32, "slot_map", slot_map)
     if rows != T or slot_map.numel() != T:
         raise ValueError("K, V and slot_map must have the same number of rows")
     if cache.device != device:
@@ -642,16 +642,16 @@ def bi_paged_decode_attention(cache: KvCache, Q, block_table, seq_lens, O, scale
     B, ldq = _heads_rows("Q", Q, device, Hq, cache.head_dim)
     rows, ldo = _heads_rows("O", O, device, Hq, cache.head_dim)
     table_rows, width, ld = _block_table(block_table, device)
-    _require(device, torch.int32, seq_lens=seq_lens)
+    _require(device, torch.int32, "seq_lens", seq_lens)
     if rows != B or table_rows != B or seq_lens.numel() != B:
         raise ValueError("Q, O, block_table and seq_lens must have the same number of rows")
     if lse is not None:
-        _require(device, torch.float32, lse=lse)
+        _require(device, torch.float32, "lse", lse)
         if lse.shape != (B, Hq):
             raise TypeError("lse must be [B, Hq]")
     nbytes = 0
     if workspace is not None:
-        _require(device, workspace.dtype, workspace=workspace)
+        _require(device, workspace.dtype, "workspace", workspace)
         nbytes = workspace.numel() * workspace.element_size()
     if cache.device != device:
         raise ValueError(f"the cache must be on the current device cuda:{device}")

@@ -39,7 +39,7 @@ extern "C" {
  * layouts; a slot, the number of one token's place, is p * page_size + i.
  * Limits: page_size 16, 32, 64, 128 or 256; head_dim 64 or 128; num_pages * page_size < 2^31.
  * k, v 16-byte aligned, strides multiples of 16 and at least head_dim, page_stride at least the
- * bytes a page spans; scales 4-byte aligned, [num_pages][num_heads].
+ * bytes a page spans, and no two codes at one byte; scales 4-byte aligned, [num_pages][num_heads].
  */
 typedef struct {
     void *k, *v;                 /* e4m3 codes */
@@ -110,8 +110,8 @@ bi_status_t bi_kv_block_tables(const int32_t *ctx_lens, const int32_t *new_lens,
  *
  * Contract: the slots of one page in one call are consecutive rows with consecutive slots, as
  * bi_kv_block_tables gives them (one run per page), and the places before a run's first slot hold
- * tokens already written.  Otherwise the page's contents are unspecified (nothing is written
- * outside the named pages).
+ * tokens that this call has written before, under a scale it has written.  Otherwise the page's
+ * contents are unspecified (nothing is written outside the named pages).
  * K and V 16-byte aligned, ldk and ldv multiples of 8 and >= num_heads * head_dim; slot_map int32
  * [T], 4-byte aligned.  T = 0 is a no-op returning BI_OK.  T < 2^31.
  * Errors: BI_ERR_INVALID_ARG, BI_ERR_ALIGNMENT, BI_ERR_UNSUPPORTED_SHAPE, BI_ERR_NO_DEVICE,

@@ -43,6 +43,10 @@ inline bi_status_t check_cache(const bi_kv_cache_t *c)
         return BI_ERR_UNSUPPORTED_SHAPE;
     if (c->page_stride < (c->page_size - 1) * c->token_stride + (c->num_heads - 1) * c->head_stride + d)
         return BI_ERR_INVALID_ARG;
+    // a token's heads beside one another, or a head's tokens: anything else overlaps
+    if (c->num_heads > 1 && c->token_stride < (c->num_heads - 1) * c->head_stride + d &&
+        c->head_stride < (c->page_size - 1) * c->token_stride + d)
+        return BI_ERR_INVALID_ARG;
     if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4) ||
         c->token_stride % 16 || c->head_stride % 16 || c->page_stride % 16)
         return BI_ERR_ALIGNMENT;

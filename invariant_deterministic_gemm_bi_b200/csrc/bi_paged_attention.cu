@@ -99,7 +99,8 @@ struct AttnArgs {
     float scale;
 };
 
-// What of a sequence is attended: positions [lo, hi), in steps from `first`.
+// What of a sequence is attended: positions [lo, hi), in steps from `first`.  A sequence without any,
+// or of a length out of range, has no chunks.
 struct Span {
     int lo, hi, first, steps, per_chunk, chunks;
     bool bad;
@@ -115,7 +116,6 @@ __device__ __forceinline__ Span span_of(int len, const AttnArgs &a)
     s.lo = a.window > 0 && s.hi > a.window ? s.hi - static_cast<int>(a.window) : 0;
     s.first = s.lo / kStep;
     s.steps = (s.hi + kStep - 1) / kStep - s.first;
-    s.steps = s.steps < 1 ? 1 : s.steps;   // an empty sequence is one empty step
     s.per_chunk = chunk_steps(s.steps);
     s.chunks = (s.steps + s.per_chunk - 1) / s.per_chunk;
     return s;
@@ -124,7 +124,7 @@ __device__ __forceinline__ Span span_of(int len, const AttnArgs &a)
 // How many chunks of class c a span has: its whole chunks, and a shorter last one.
 __device__ __forceinline__ int chunks_of_class(const Span &s, int c)
 {
-    const int whole = s.steps / s.per_chunk, rest = s.steps - whole * s.per_chunk;
+    const int whole = s.steps / s.per_chunk, rest = s.steps - whole * s.per_chunk;   // 0 of both without steps
     return (class_of(s.per_chunk) == c ? whole : 0) + (rest > 0 && class_of(rest) == c ? 1 : 0);
 }
 
@@ -221,7 +221,7 @@ struct Item {
     int b, kvh;          // b < 0: no more items
     int lo, hi;          // the sequence's attended positions
     int key0, steps;     // the chunk's first position and length
-    int chunk, chunks;   // chunk < 0: the sequence's length is out of range
+    int chunk, chunks;
 };
 static_assert(sizeof(Item) == 32, "two 16-byte words");
 
@@ -333,7 +333,7 @@ __device__ __forceinline__ Item make_item(const AttnArgs &a, const S &sm, int i)
     it.hi = s.hi;
     it.key0 = (s.first + chunk * s.per_chunk) * kStep;
     it.steps = min(s.per_chunk, s.steps - chunk * s.per_chunk);
-    it.chunk = s.bad ? -1 : chunk;
+    it.chunk = chunk;
     it.chunks = s.chunks;
     return it;
 }
@@ -726,22 +726,46 @@ __device__ __forceinline__ void add_states(Shared<D, MG> &sm, const AttnArgs &a,
         }
         const int h = it.kvh * a.group + head;
         const int64_t row = static_cast<int64_t>(it.b) * a.hq + h;
-        const bool bad = it.chunk < 0 || *static_cast<volatile int *>(&sm.dead), empty = it.hi <= it.lo;
+        const bool dead = *static_cast<volatile int *>(&sm.dead) != 0;
         if (it.chunks == 1) {
-            const float r = bad ? NAN : empty ? 0.0f : 1.0f / sum;
-            if (empty || bad)
-                acc = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+            const float r = dead ? NAN : 1.0f / sum;
             uint2 y;
             *reinterpret_cast<__nv_bfloat162 *>(&y.x) = __floats2bfloat162_rn(acc.x * r, acc.y * r);
             *reinterpret_cast<__nv_bfloat162 *>(&y.y) = __floats2bfloat162_rn(acc.z * r, acc.w * r);
             *reinterpret_cast<uint2 *>(a.out + it.b * a.ldo + static_cast<int64_t>(h) * D + dd) = y;
             if (a.lse && dd == 0)
-                a.lse[row] = bad ? NAN : empty ? -INFINITY : (mx - kWeightExp + log2f(sum)) * kLn2;
+                a.lse[row] = dead ? NAN : (mx - kWeightExp + log2f(sum)) * kLn2;
         } else {
             const int64_t at = row * a.chunks + it.chunk;
             *reinterpret_cast<float4 *>(a.part + at * D + dd) = acc;
             if (dd == 0)
-                a.part_ml[at] = make_float2(mx, bad ? NAN : sum);
+                a.part_ml[at] = make_float2(mx, dead ? NAN : sum);
+        }
+    }
+}
+
+// The outputs of sequences that have no chunks: 0 and -inf, or NaN.  CTA c looks at sequences c, c +
+// gridDim, ..., 32 a warp at a time.  (In a padded batch they would cost an item for each head.)
+template <int D>
+__device__ __forceinline__ void fill_empty(const AttnArgs &a, int w)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kHelpers;
+    for (int64_t b0 = blockIdx.x + static_cast<int64_t>(gridDim.x) * w; b0 < a.b; b0 += 32 * step) {
+        const int64_t mine = b0 + lane * step;
+        const int len = mine < a.b ? a.lens[mine] : 1;
+        const bool bad = mine < a.b && (len < 0 || len > a.max_len);
+        const uint32_t bads = __ballot_sync(kFull, bad);
+        for (uint32_t todo = __ballot_sync(kFull, bad || len == 0); todo != 0; todo &= todo - 1) {
+            const int l = __ffs(todo) - 1;
+            const int64_t b = b0 + l * step;
+            const bool nan = (bads >> l) & 1u;
+            const uint32_t y = nan ? 0x7fff7fffu : 0u;   // two bf16
+            for (int x = lane; x < a.hq * D / 8; x += 32)
+                reinterpret_cast<uint4 *>(a.out + b * a.ldo)[x] = make_uint4(y, y, y, y);
+            if (a.lse)
+                for (int x = lane; x < a.hq; x += 32)
+                    a.lse[b * a.hq + x] = nan ? NAN : -INFINITY;
         }
     }
 }
@@ -756,6 +780,7 @@ __device__ __forceinline__ void help(Shared<D, MG> &sm, const AttnArgs &a, int w
         q.store(sm, a, i, w);
         warp_arrive(&sm.helped[i]);
     }
+    fill_empty<D>(a, w);
     for (int i = 0;; ++i) {
         const Item now = sm.items[i % kItemRing];
         if (now.b < 0)
@@ -882,8 +907,8 @@ __global__ void __launch_bounds__(kWide < 8 ? 256 : 32 * kWide) paged_merge_kern
     bi_kv::dependency_wait();
     const bool real = row < static_cast<int64_t>(a.b) * a.hq;
     const int b = real ? static_cast<int>(row / a.hq) : 0;
-    const int chunks = real ? span_of(a.lens[b], a).chunks : 1;
-    const int eights = chunks == 1 ? 0 : (chunks + kEight - 1) / kEight;
+    const int chunks = real ? span_of(a.lens[b], a).chunks : 0;
+    const int eights = chunks <= 1 ? 0 : (chunks + kEight - 1) / kEight;
     for (int e = w; e < eights; e += kWide) {
         const float2 *ml = a.part_ml + row * a.chunks + e * kEight;
         const float *part = a.part + (row * a.chunks + e * kEight) * D + lane * kVec;

@@ -260,3 +260,77 @@ def test_many_items_per_block(heads, lens):
     one, one_lse = attend(P.cache, Q, P.dtable, P.dlens, 0.125)
     assert torch.equal(O.view(torch.int16), one.view(torch.int16)[row]) and torch.equal(lse, one_lse[row])
     check(P, 2 * heads, heads, 64, seed=19, scale=0.125)
+
+
+def test_padded_batches_and_empty_tables():
+    # a captured batch of 300 slots with a handful in use: the others' rows are zero, or NaN where the
+    # length is out of range, and the ones in use do not see them
+    P = Paged([700, 3, 260, 1100], 4, 128, 16, seed=970)
+    at = [0, 17, 150, 299]
+    B = 300
+    lens = torch.zeros(B, dtype=torch.int32, device=DEV)
+    table = torch.full((B, P.width), -1, dtype=torch.int32, device=DEV)
+    Q = queries(B, 16, 128, 20)
+    lens[at], table[at] = P.dlens, P.dtable
+    lens[5], lens[200] = -3, 16 * P.width + 1
+    O, lse = attend(P.cache, Q, table, lens, 0.1)
+    want, wlse = attend(P.cache, Q[at].contiguous(), P.dtable, P.dlens, 0.1)
+    assert torch.equal(O[at].view(torch.int16), want.view(torch.int16)) and torch.equal(lse[at], wlse)
+    assert torch.isnan(O[[5, 200]].float()).all() and torch.isnan(lse[[5, 200]]).all()
+    rest = [b for b in range(B) if b not in at + [5, 200]]
+    assert torch.all(O[rest] == 0) and torch.isneginf(lse[rest]).all()
+    # no pages at all
+    none = torch.empty((B, 0), dtype=torch.int32, device=DEV)
+    lens.zero_()
+    lens[7] = 1
+    O, lse = attend(P.cache, Q, none, lens, 0.1)
+    assert torch.isnan(O[7].float()).all() and torch.all(O[:7] == 0) and torch.all(O[8:] == 0)
+
+
+def test_two_calls_at_once_with_workspaces_of_their_own():
+    P = Paged([3000, 40, 900, 2500], 4, 128, 32, seed=980)
+    Qs = [queries(4, 16, 128, 21 + i) for i in range(2)]
+    want = [attend(P.cache, Q, P.dtable, P.dlens, 0.1)[0] for Q in Qs]
+    n = bg.bi_paged_decode_attention_workspace_bytes(4, 16, 128, P.width * 32)
+    ws = [torch.empty(n, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    outs = [torch.empty_like(Q) for Q in Qs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                bg.bi_paged_decode_attention(P.cache, Qs[i], P.dtable, P.dlens, outs[i], 0.1, workspace=ws[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(outs[i].view(torch.int16), want[i].view(torch.int16))
+
+
+def test_back_to_back_steps_in_one_stream_order():
+    # write, attend, overwrite and attend again with nothing between them: each attention reads what
+    # the write before it left, and the next write does not overtake it
+    page, heads, D = 32, 2, 128
+    k, v = pool(4, page, heads, D, fill=0), pool(4, page, heads, D, fill=0)
+    one = torch.ones((4, heads), device=DEV)
+    cache = bg.KvCache(k, v, one, one.clone())
+    table = torch.tensor([[2, 0, 3]], dtype=torch.int32, device=DEV)
+    slots = torch.tensor([2 * page + i for i in range(page)] + [i for i in range(page)] + [3 * page + i for i in range(9)],
+                         dtype=torch.int32, device=DEV)
+    n = torch.tensor([2 * page + 9], dtype=torch.int32, device=DEV)
+    K = [inputs.bf16_gaussian((2 * page + 9, heads, D), seed=900 + i, device=DEV) for i in range(6)]
+    Q = queries(1, 8, D, 22)
+    def run(sync):
+        outs = []
+        for i in range(6):
+            bg.bi_kv_append_e4m3(cache, K[i], K[5 - i], slots)
+            if sync:
+                torch.cuda.synchronize()
+            O = torch.empty((1, 8, D), dtype=torch.bfloat16, device=DEV)
+            bg.bi_paged_decode_attention(cache, Q, table, n, O, 0.1)
+            if sync:
+                torch.cuda.synchronize()
+            outs.append(O)
+        return torch.stack(outs)
+    apart = run(True)
+    assert len({tuple(o.flatten()[:16].tolist()) for o in apart}) == 6
+    for _ in range(5):
+        assert torch.equal(run(False).view(torch.int16), apart.view(torch.int16))

@@ -26,6 +26,7 @@ CACHES = [({"k": None}, BAD), ({"v": None}, BAD), ({"k_scale": None}, BAD), ({"v
           ({"page_stride": 15 * 256}, BAD), ({"page_stride": -4096}, BAD), ({"token_stride": 2 ** 62}, SHAPE),
           ({"head_stride": 2 ** 62}, SHAPE), ({"page_stride": 2 ** 62}, SHAPE), ({"k": 264}, ALIGN), ({"v": 8}, ALIGN),
           ({"k_scale": 258}, ALIGN), ({"page_stride": 4104}, ALIGN), ({"token_stride": 264, "page_stride": 8192}, ALIGN),
+          ({"head_stride": 256, "token_stride": 128, "page_stride": 8192}, BAD), ({"token_stride": 128}, BAD),
           ({"head_stride": 136, "token_stride": 272, "page_stride": 8192}, ALIGN)]
 
 

@@ -515,19 +515,23 @@ def _require(device, dtype, names, *tensors):
             raise TypeError(f"{name} must be a contiguous {dtype} tensor")
 
 
-def _current_device() -> int:
+def _current_device(torch) -> int:
     """The current device's number; -1, the device number of CPU tensors' get_device(), without one
     (argument checks then run to their end and the C call reports BI_ERR_NO_DEVICE)."""
-    import torch
     try:
         return torch.cuda.current_device()
     except (AssertionError, RuntimeError):
         return -1
 
 
-def _heads_rows(name, x, device, heads, dim):
+def _stream_on(torch, device, stream):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device) if device >= 0 else None
+    return _stream_handle(stream)
+
+
+def _heads_rows(torch, name, x, device, heads, dim):
     """(rows, row pitch) of bf16 [rows, heads, dim] whose rows are contiguous, of any pitch."""
-    import torch
     if x.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be bf16")
     shape, stride = x.shape, x.stride()
@@ -541,12 +545,12 @@ def _heads_rows(name, x, device, heads, dim):
     return rows, (stride[0] if rows > 1 else heads * dim)
 
 
-def _block_table(table, device):
+def _block_table(torch, table, device):
     """(rows, width, row pitch) of a block table."""
-    import torch
-    if table.dtype is not torch.int32 or table.dim() != 2:
+    shape, stride = table.shape, table.stride()
+    if table.dtype is not torch.int32 or len(shape) != 2:
         raise TypeError("block_table must be int32 [B, max_pages]")
-    (rows, width), stride = table.shape, table.stride()
+    rows, width = shape
     if width > 1 and stride[1] != 1:
         raise TypeError("block_table must have a unit inner stride")
     if table.get_device() != device:
@@ -594,12 +598,12 @@ def bi_kv_block_tables(ctx_lens, new_lens, page_size: int, free_pages, free_coun
     pages; block_table [B, max_pages]; token_offsets [B+1]; slot_map, positions [max_tokens];
     free_left, status [1].  seq_lens may be ctx_lens and free_left may be free_count."""
     import torch
-    device = _current_device()
+    device = _current_device(torch)
     _require(device, torch.int32, "ctx_lens new_lens free_pages free_count seq_lens token_offsets slot_map "
              "free_left status positions", ctx_lens, new_lens, free_pages, free_count, seq_lens, token_offsets,
              slot_map, free_left, status, positions)
     B, tokens = ctx_lens.numel(), slot_map.numel()
-    rows, width, ld = _block_table(block_table, device)
+    rows, width, ld = _block_table(torch, block_table, device)
     if rows != B or new_lens.numel() != B or seq_lens.numel() != B or token_offsets.numel() != B + 1 or \
             free_count.numel() != 1 or free_left.numel() != 1 or status.numel() != 1 or \
             (positions is not None and positions.numel() != tokens):
@@ -608,22 +612,22 @@ def bi_kv_block_tables(ctx_lens, new_lens, page_size: int, free_pages, free_coun
         ctx_lens.data_ptr(), new_lens.data_ptr(), B, page_size, free_pages.data_ptr(), free_pages.numel(),
         free_count.data_ptr(), block_table.data_ptr(), ld, width, seq_lens.data_ptr(),
         token_offsets.data_ptr(), slot_map.data_ptr(), _ptr(positions), tokens, free_left.data_ptr(),
-        status.data_ptr(), _stream_handle(stream)), "bi_kv_block_tables")
+        status.data_ptr(), _stream_on(torch, device, stream)), "bi_kv_block_tables")
 
 
 def bi_kv_append_e4m3(cache: KvCache, K, V, slot_map, stream=None):
     """Write bf16 K, V [T, heads, head_dim] (rows of any pitch) to the slots slot_map int32 [T]."""
     import torch
-    device = _current_device()
-    T, ldk = _heads_rows("K", K, device, cache.num_heads, cache.head_dim)
-    rows, ldv = _heads_rows("V", V, device, cache.num_heads, cache.head_dim)
+    device = _current_device(torch)
+    T, ldk = _heads_rows(torch, "K", K, device, cache.num_heads, cache.head_dim)
+    rows, ldv = _heads_rows(torch, "V", V, device, cache.num_heads, cache.head_dim)
     _require(device, torch.int32, "slot_map", slot_map)
     if rows != T or slot_map.numel() != T:
         raise ValueError("K, V and slot_map must have the same number of rows")
     if cache.device != device:
         raise ValueError(f"the cache must be on the current device cuda:{device}")
     _check(load_library().bi_kv_append_e4m3(cache.ref, K.data_ptr(), ldk, V.data_ptr(), ldv,
-                                            slot_map.data_ptr(), T, _stream_handle(stream)),
+                                            slot_map.data_ptr(), T, _stream_on(torch, device, stream)),
            "bi_kv_append_e4m3")
 
 
@@ -637,11 +641,11 @@ def bi_paged_decode_attention(cache: KvCache, Q, block_table, seq_lens, O, scale
     and, if given, lse fp32 [B, Hq].  workspace: a contiguous device tensor of at least
     bi_paged_decode_attention_workspace_bytes(B, Hq, D, max_pages * page_size) bytes."""
     import torch
-    device = _current_device()
+    device = _current_device(torch)
     Hq = Q.shape[1]
-    B, ldq = _heads_rows("Q", Q, device, Hq, cache.head_dim)
-    rows, ldo = _heads_rows("O", O, device, Hq, cache.head_dim)
-    table_rows, width, ld = _block_table(block_table, device)
+    B, ldq = _heads_rows(torch, "Q", Q, device, Hq, cache.head_dim)
+    rows, ldo = _heads_rows(torch, "O", O, device, Hq, cache.head_dim)
+    table_rows, width, ld = _block_table(torch, block_table, device)
     _require(device, torch.int32, "seq_lens", seq_lens)
     if rows != B or table_rows != B or seq_lens.numel() != B:
         raise ValueError("Q, O, block_table and seq_lens must have the same number of rows")
@@ -657,6 +661,6 @@ def bi_paged_decode_attention(cache: KvCache, Q, block_table, seq_lens, O, scale
         raise ValueError(f"the cache must be on the current device cuda:{device}")
     _check(load_library().bi_paged_decode_attention(
         cache.ref, Q.data_ptr(), ldq, block_table.data_ptr(), ld, width, seq_lens.data_ptr(), B, Hq, scale,
-        window, _ptr(workspace), nbytes, O.data_ptr(), ldo, _ptr(lse), _stream_handle(stream)),
+        window, _ptr(workspace), nbytes, O.data_ptr(), ldo, _ptr(lse), _stream_on(torch, device, stream)),
         "bi_paged_decode_attention")
     return O

@@ -907,27 +907,39 @@ __global__ void __launch_bounds__(kWide < 8 ? 256 : 32 * kWide) paged_merge_kern
     bi_kv::dependency_wait();
     const bool real = row < static_cast<int64_t>(a.b) * a.hq;
     const int b = real ? static_cast<int>(row / a.hq) : 0;
-    const int chunks = real ? span_of(a.lens[b], a).chunks : 0;
-    const int eights = chunks <= 1 ? 0 : (chunks + kEight - 1) / kEight;
-    for (int e = w; e < eights; e += kWide) {
+    float v[kEight][kVec];
+    float2 x[kEight];
+    auto load_eight = [&](int e, int limit) {   // parts below the limit; the others stay what they are
         const float2 *ml = a.part_ml + row * a.chunks + e * kEight;
         const float *part = a.part + (row * a.chunks + e * kEight) * D + lane * kVec;
-        float v[kEight][kVec];
-        float2 x[kEight];
 #pragma unroll
-        for (int j = 0; j < kEight; ++j) {
-            x[j] = make_float2(-INFINITY, 0.0f);
-#pragma unroll
-            for (int i = 0; i < kVec; ++i)
-                v[j][i] = 0.0f;
-            if (e * kEight + j < chunks) {
+        for (int j = 0; j < kEight; ++j)
+            if (e * kEight + j < limit) {
                 x[j] = ml[j];
                 if constexpr (kVec == 4)
                     *reinterpret_cast<float4 *>(v[j]) = *reinterpret_cast<const float4 *>(part + j * D);
                 else
                     *reinterpret_cast<float2 *>(v[j]) = *reinterpret_cast<const float2 *>(part + j * D);
             }
-        }
+    };
+    // With at most eight chunks the parts are asked for before the length is known; those of chunks
+    // that the sequence does not have (never written, or by an earlier call) are not used.
+    if constexpr (kWide == 1)
+        if (real)
+            load_eight(0, a.chunks);
+    const int chunks = real ? span_of(a.lens[b], a).chunks : 0;
+    const int eights = chunks <= 1 ? 0 : (chunks + kEight - 1) / kEight;
+    for (int e = w; e < eights; e += kWide) {
+        if constexpr (kWide > 1)
+            load_eight(e, chunks);
+#pragma unroll
+        for (int j = 0; j < kEight; ++j)
+            if (e * kEight + j >= chunks) {
+                x[j] = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+                for (int i = 0; i < kVec; ++i)
+                    v[j][i] = 0.0f;
+            }
         float mx = -INFINITY, sum = 0.0f, acc[kVec] = {};
 #pragma unroll
         for (int j = 0; j < kEight; ++j)
@@ -1021,11 +1033,12 @@ bi_status_t run_attention(const AttnArgs &a, const CUtensorMap &k_map, const CUt
                                   k_map, v_map, a);
     if (st != BI_OK || a.chunks == 1)
         return st;
-    // Warps for a head: one where no sequence can have more than eight chunks; else four, or sixteen
+    // Warps for a head: one or two where no sequence can have more eights of chunks; else four, or sixteen
     // (all eights at once) while there are so few heads that all warps are resident (2 x 100001,
-    // 64 heads: 3.7 us against 11 us with four; 3200 ragged heads: 13 us against 8 us).
+    // 64 heads: the call takes 73.4 us, with four 76.0; 3200 ragged heads: 58.6 us, with four 50.9).
     const int eights = (a.chunks + kEight - 1) / kEight;
-    return eights <= 1                                                            ? run_merge<D, 1>(a, stream)
+    return eights <= 1   ? run_merge<D, 1>(a, stream)
+           : eights <= 2 ? run_merge<D, 2>(a, stream)
            : eights <= 4 || static_cast<int64_t>(a.b) * a.hq > INT64_C(4) * sms ? run_merge<D, 4>(a, stream)
                                                                                   : run_merge<D, 16>(a, stream);
 }

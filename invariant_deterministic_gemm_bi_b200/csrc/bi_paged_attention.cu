@@ -387,12 +387,14 @@ __device__ __forceinline__ void produce(Shared<D, MG> &sm, const AttnArgs &a, co
 
     int slot = 0;
     uint32_t parity = 1;     // of a stage not used yet
+    bool used_all = false;   // every stage has been used
     auto take_slot = [&]() { wait_for(sm, &sm.empty[slot], parity); };
     auto give_slot = [&]() {
         warp_arrive(&sm.full[slot]);   // releases the words stored for it
         if (++slot == S::kStages) {
             slot = 0;
             parity ^= 1;
+            used_all = true;
         }
     };
 
@@ -448,6 +450,12 @@ __device__ __forceinline__ void produce(Shared<D, MG> &sm, const AttnArgs &a, co
             sm.stage[slot] = {0, 0, 0, kEnd};
         give_slot();
     }
+    // Consumers wait for every stage, unless a wait has given up: then copies may be in flight still.
+    // The last use of a stage before `slot` was in this round of the ring, of the others in the round before.
+    if (*static_cast<volatile int *>(&sm.dead))
+        for (int i = 0; i < S::kStages; ++i)
+            if (i < slot || used_all)
+                bi::ptx::mbar_wait(&sm.full[i], i < slot ? parity ^ 1 : parity, kWaitCycles, nullptr);
 }
 
 template <int D, int MG>

@@ -239,9 +239,9 @@ __global__ void __launch_bounds__(kTableThreads, 1) kv_tables_kernel(TableArgs a
 // ---------------------------------------------------------------------------------------------
 // The write into the cache.  A run -- rows with consecutive slots of one page -- has at most
 // page_size tokens.  A group of warps, one for each 16 tokens of a page (eight for pages of 256), takes
-// one head of K or of V and the runs that begin in a block of up to 16 rows (32): all those that end
-// within as many rows of the block's first together in one warp (a decode step's are one token
-// each), then a share of the one run that does not a warp.  The tokens stay in registers between the
+// one head of K or of V and the runs that begin in a block of up to 32 rows: those inside the first 16
+// rows together in one warp, and those inside the other 16 (a decode step's are one token each), then
+// the remaining ones in turn, a share of the page a warp.  The tokens stay in registers between the
 // pass that finds the largest magnitudes and the one that rounds.  Only when a page's exponent grows
 // are its earlier codes read and moved.  The warps of a CTA take neighbouring heads, whose rows lie
 // side by side.  Memory bound for prompts, latency bound for a decode step.
@@ -411,14 +411,14 @@ __device__ __forceinline__ void write_huge(uint8_t *to, const uint4 *from, float
     }
 }
 
-// G warps a group, kPiece tokens a warp and rows a block: G * kPiece = page_size.
+// G warps a group, kPiece tokens a warp: G * kPiece = page_size.
 template <int D, int G, int kPiece>
 __global__ void __launch_bounds__(32 * kAppendWarps, kPiece == 16 ? 3 : 2) kv_append_kernel(const __grid_constant__ AppendArgs a)
 {
     constexpr int kVecs = D / 8;             // 16-byte vectors of a row's head
     constexpr int kTokens = 32 / kVecs;      // tokens one load instruction covers
     constexpr int kLoads = kPiece / kTokens;
-    __shared__ uint32_t top_s[kAppendWarps];
+    __shared__ uint32_t top_s[2][kAppendWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int group = warp / G, part = warp % G;
     const int page = 1 << a.page_shift;
@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kPiece == 16 ? 3 : 2) kv_ap
 
     // The slots of the block's rows and of a page of rows behind them, all asked for at once.  Bit l of
     // follows[k]: row t0 + 32 k + l continues the run of the row before.
-    constexpr int kWords = (G * kPiece + kPiece + 31) / 32 + 1;
+    constexpr int kWords = (G * kPiece + 31) / 32 + 1;
     int mine[kWords];
 #pragma unroll
     for (int k = 0; k < kWords; ++k) {
@@ -467,19 +467,24 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kPiece == 16 ? 3 : 2) kv_ap
     const uint32_t breaks = lane == 31 ? 0u : ~follows[0] >> (lane + 1);
     const int end = breaks != 0 ? lane + __ffs(breaks) : (follows[1] & 1u) ? 33 : 32;
     const bool ours = start >= 0 && ((block >> start) & 1u);
-    const uint32_t here = __ballot_sync(kFull, ours && end <= kPiece);   // rows of runs that end in sight
-    const uint32_t on = __ballot_sync(kFull, ours && end > kPiece);      // of the one that goes on
+    const bool inside = ours && end <= start / kPiece * kPiece + kPiece;   // its kPiece rows
+    const uint32_t short_rows = __ballot_sync(kFull, inside);
+    uint32_t on = __ballot_sync(kFull, ours && lane == start && !inside);   // first rows of the others
 
-    if (part == 0 && here != 0) {
+#pragma unroll 1
+    for (int row0 = 0; row0 < 32; row0 += kPiece) {   // the first warp's work
+        const uint32_t here = kPiece == 32 ? short_rows : short_rows >> row0 & ((1u << (kPiece & 31)) - 1u);
+        if (part != 0 || here == 0)
+            continue;
         uint4 v[kLoads];
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
             const int tok = j * kTokens + lane / kVecs;
             v[j] = make_uint4(0, 0, 0, 0);
             if ((here >> tok) & 1u)
-                v[j] = __ldg(reinterpret_cast<const uint4 *>(x + tok * ld));
+                v[j] = __ldg(reinterpret_cast<const uint4 *>(x + (row0 + tok) * ld));
         }
-        const bool used = (here >> lane) & 1u, leads = used && lane == start;
+        const bool used = lane >= row0 && lane < row0 + kPiece && ((short_rows >> lane) & 1u), leads = used && lane == start;
         const int slot = mine[0], off = slot & (page - 1);
         float *scale = scales + static_cast<int64_t>(slot >> a.page_shift) * a.heads;
         const uint32_t old_scale = leads && off != 0 ? __float_as_uint(*scale) : 0u;
@@ -497,7 +502,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kPiece == 16 ? 3 : 2) kv_ap
                 for (int m = kVecs / 2; m > 0; m >>= 1)
                     y = max(y, __shfl_xor_sync(kFull, y, m));
                 y = __shfl_sync(kFull, y, lane % kTokens * kVecs);
-                top = lane / kTokens == j ? y : top;
+                top = (lane - row0) / kTokens == j ? y : top;
             }
         // the run's largest, at its last row and from there to all of it
 #pragma unroll
@@ -522,8 +527,8 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kPiece == 16 ? 3 : 2) kv_ap
         if (leads)
             *scale = pow2(e);
         auto place = [&](int tok, float *inv) {   // of token tok's 8 codes
-            const int to = __shfl_sync(kFull, slot, tok);
-            *inv = pow2(-__shfl_sync(kFull, e, tok));
+            const int to = __shfl_sync(kFull, slot, row0 + tok);
+            *inv = pow2(-__shfl_sync(kFull, e, row0 + tok));
             return pool + static_cast<int64_t>(to >> a.page_shift) * a.page_stride + (to & (page - 1)) * a.token_stride +
                    lane % kVecs * 8;
         };
@@ -543,11 +548,13 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kPiece == 16 ? 3 : 2) kv_ap
                 float inv;
                 uint8_t *to = place(tok, &inv);
                 if ((here >> tok) & 1u)
-                    write_huge(to, reinterpret_cast<const uint4 *>(x + tok * ld), inv);
+                    write_huge(to, reinterpret_cast<const uint4 *>(x + (row0 + tok) * ld), inv);
             }
     }
 
-    if (on != 0) {
+    int turn = 0;
+#pragma unroll 1
+    for (; on != 0; on &= on - 1, turn ^= 1) {
         const int i = __ffs(on) - 1;   // the run's first row
         int n = 32 * kWords - i;       // up to the first row behind it that does not follow
 #pragma unroll
@@ -586,11 +593,11 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kPiece == 16 ? 3 : 2) kv_ap
         top = __reduce_max_sync(kFull, top);
         if constexpr (G > 1) {
             if (lane == 0)
-                top_s[warp] = top;
+                top_s[turn][warp] = top;
             group_sync<G>(group);   // also: every warp has read the scale
 #pragma unroll
             for (int w = 0; w < G; ++w)
-                top = max(top, top_s[group * G + w]);
+                top = max(top, top_s[turn][group * G + w]);
         }
         int e = exponent_of(top);
         if (off != 0) {
@@ -736,12 +743,12 @@ bi_status_t bi_kv_append_e4m3(const bi_kv_cache_t *cache, const void *K, int64_t
     a.heads = cache->num_heads;
     a.page_shift = bi_kv::log2_of(cache->page_size);
     // Rows per block: one, so that the runs of a decode step are written side by side, while all warps
-    // are resident at once (64 tokens, 8 heads, pages of 64: two rows 3.1 us, one 4.9 us); at most what
-    // a warp holds.
+    // are resident at once (64 tokens, 8 heads, pages of 64: two rows 3.1 us, one 4.9 us); at most a
+    // warp's 32.
     const int64_t groups = 2 * static_cast<int64_t>(cache->num_heads);
-    const int most_rows = cache->page_size == 256 ? 32 : 16, warps = cache->page_size == 256 ? 8 : cache->page_size / 16;
+    const int warps = cache->page_size == 256 ? 8 : cache->page_size / 16;
     a.rows = 1;
-    while (a.rows < most_rows && (T + a.rows - 1) / a.rows * groups * warps > 24 * static_cast<int64_t>(sms))
+    while (a.rows < 32 && (T + a.rows - 1) / a.rows * groups * warps > 24 * static_cast<int64_t>(sms))
         a.rows *= 2;
     const int64_t blocks = (T + a.rows - 1) / a.rows;
     if (blocks > INT32_MAX / groups)

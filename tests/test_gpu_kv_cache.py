@@ -257,6 +257,24 @@ def test_many_single_tokens_and_no_tokens():
     bg.bi_kv_append_e4m3(cache, empty, empty, ints([]))
 
 
+@pytest.mark.parametrize("page,heads,dim,B", [(128, 2, 64, 1200), (16, 2, 128, 2500), (256, 1, 64, 900)])
+def test_large_steps_of_single_tokens_and_pieces(page, heads, dim, B):
+    # so many rows that a block holds 32 of them: single tokens beside runs of a few, runs that cross
+    # the middle of a block and its end, and skipped rows, each request in a page of its own
+    g = np.random.default_rng(page + B)
+    cache = fresh(B, page, heads, dim)
+    cache.k.copy_(inputs.e4m3_gaussian(cache.k.shape, 91, DEV).view(torch.uint8))
+    cache.v.copy_(inputs.e4m3_gaussian(cache.v.shape, 92, DEV).view(torch.uint8))
+    cache.k_scale.copy_(inputs.scales_pow2((B, heads), 93, lo=-6, hi=2, device=DEV))
+    cache.v_scale.copy_(inputs.scales_pow2((B, heads), 94, lo=-6, hi=2, device=DEV))
+    slots = []
+    for p in g.permutation(B):
+        n = min(int(g.choice([1, 1, 1, 1, 2, 3, 5, 17, 40])), page)
+        off = int(g.integers(0, page - n + 1)) if g.random() < 0.8 else 0
+        slots += [int(p) * page + off + i for i in range(n)] + [-1] * int(g.integers(0, 2))
+    write_and_compare(cache, tokens(len(slots), heads, dim, 95, 2.0), tokens(len(slots), heads, dim, 97, 2.0), slots)
+
+
 def test_slots_beyond_32_bits_of_codes():
     page, heads, dim = 256, 8, 128
     pages = (9 << 29) // (page * heads * dim)

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <mutex>
 
 #include "bi_kv_cache.h"
 #include "bi_kv_common.cuh"
@@ -234,6 +235,26 @@ __global__ void __launch_bounds__(kTableThreads, 1) kv_tables_kernel(TableArgs a
         *a.free_left = static_cast<int32_t>(top - need);
         *a.status = BI_OK;
     }
+}
+
+size_t table_smem_bytes(int64_t b) { return (4 * static_cast<size_t>(b) + 3) * sizeof(int32_t); }
+
+// Once per device: shared memory for the most requests, whatever this call has, since host threads
+// that each set their own call's amount would undo one another's.
+bi_status_t prepare_tables(int dev)
+{
+    static std::mutex mu;
+    static bool done[bi_kv::kMaxDevices] = {};
+    std::lock_guard<std::mutex> lock(mu);
+    if (!done[dev]) {
+        if (cudaFuncSetAttribute(kv_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(table_smem_bytes(kMaxRequests))) != cudaSuccess) {
+            cudaGetLastError();
+            return BI_ERR_CUDA;
+        }
+        done[dev] = true;
+    }
+    return BI_OK;
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -692,12 +713,10 @@ bi_status_t bi_kv_block_tables(const int32_t *ctx_lens, const int32_t *new_lens,
     a.max_tokens = max_tokens;
     a.b = static_cast<int>(B);
     a.page_shift = bi_kv::log2_of(page_size);
-    const size_t smem = (4 * static_cast<size_t>(B) + 3) * sizeof(int32_t);
-    if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(kv_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) {
-        cudaGetLastError();
-        return BI_ERR_CUDA;
-    }
+    st = prepare_tables(dev);
+    if (st != BI_OK)
+        return st;
+    const size_t smem = table_smem_bytes(B);
     // CTAs: one for every 4096 tokens, up to a portable cluster
     int cluster = 1;
     while (cluster < 8 && static_cast<int64_t>(cluster) * kTableThreads * kTableTokens < (max_tokens > B ? max_tokens : B))

@@ -53,10 +53,11 @@ inline bi_status_t check_cache(const bi_kv_cache_t *c)
     return BI_OK;
 }
 
+constexpr int kMaxDevices = 64;
+
 // The current device and its SM count.  The properties are read once per device.
 inline bi_status_t current_device(int *dev_out, int *num_sms)
 {
-    constexpr int kMaxDevices = 64;
     struct Info {
         bool probed, ok;
         int sms;

@@ -1024,7 +1024,7 @@ template <int D, int MG>
 bi_status_t run_attention(const AttnArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map, int dev, int sms, cudaStream_t stream)
 {
     static std::mutex mu;
-    static bool set[64] = {};
+    static bool set[bi_kv::kMaxDevices] = {};
     static_assert(sizeof(Shared<D, MG>) <= 232448, "shared memory of an SM");
     {
         std::lock_guard<std::mutex> lock(mu);

@@ -1,5 +1,7 @@
 """The paged cache's block tables and write on the GPU, bit for bit against the oracle, and a served
 run of tables, write and attention together."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -105,6 +107,31 @@ def test_bad_page_numbers_on_the_stack_give_no_slot():
     a = ([0, 0, 0], [1, 1, 1], 256, [3, -4, 2 ** 31 - 1], 3, np.full((3, 1), -1), 3)
     s = run_tables(*a)
     assert s["slots"].tolist() == [-1, -1, 3 * 256] and s["status"].item() == 0
+
+
+def test_host_threads_with_different_numbers_of_requests():
+    """Each call needs shared memory for its own requests; one thread's amount must not become the other's."""
+    failures = []
+
+    def work(B):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                ctx, new, lens, offsets = ints([5] * B), ints([0] * B), ints([7] * B), ints([7] * (B + 1))
+                table, stack, one, slots = ints([[3]] * B), ints([4]), ints([1]), ints([7])
+                left, status = ints([7]), ints([7])
+                for _ in range(2000):
+                    bg.bi_kv_block_tables(ctx, new, 16, stack, one, table, lens, offsets, slots, left, status)
+                torch.cuda.current_stream().synchronize()
+            assert torch.all(lens == 5) and left.item() == 1 and status.item() == 0
+        except Exception as e:   # reported by the test's own thread
+            failures.append((B, e))
+
+    threads = [threading.Thread(target=work, args=(B,)) for B in (3500, 5000, 8192)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failures
 
 
 def test_lengths_and_count_in_place_under_a_replayed_graph():

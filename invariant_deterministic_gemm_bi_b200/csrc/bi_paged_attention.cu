@@ -577,13 +577,13 @@ __device__ __forceinline__ void consume(Shared<D, MG> &sm, const AttnArgs &a, in
                     mx[h] = fmaxf(mx[h], __shfl_xor_sync(kFull, mx[h], 16));
                 }
                 const float corr[2] = {exp2_approx(m[n][0] - mx[0]), exp2_approx(m[n][1] - mx[1])};
-                const float ref[2] = {mx[0] - kWeightExp, mx[1] - kWeightExp};
                 float sum[2] = {0.0f, 0.0f};
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt) {
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        s[n][mt][x] = exp2_approx(s[n][mt][x] - ref[x & 1]);
+                        // the maximum first: it may be so large that kWeightExp beside it rounds away
+                        s[n][mt][x] = exp2_approx((s[n][mt][x] - mx[x & 1]) + kWeightExp);
                         sum[x & 1] = fmaf(s[n][mt][x], rsv[mt], sum[x & 1]);
                     }
                     pf[n][mt][0] = transpose8x8(pack_half(s[n][mt][0], s[n][mt][1]));
@@ -745,7 +745,7 @@ __device__ __forceinline__ void add_states(Shared<D, MG> &sm, const AttnArgs &a,
             *reinterpret_cast<__nv_bfloat162 *>(&y.y) = __floats2bfloat162_rn(acc.z * r, acc.w * r);
             *reinterpret_cast<uint2 *>(a.out + it.b * a.ldo + static_cast<int64_t>(h) * D + dd) = y;
             if (a.lse && dd == 0)
-                a.lse[row] = dead ? NAN : (mx - kWeightExp + log2f(sum)) * kLn2;
+                a.lse[row] = dead ? NAN : (mx + (log2f(sum) - kWeightExp)) * kLn2;
         } else {
             const int64_t at = row * a.chunks + it.chunk;
             *reinterpret_cast<float4 *>(a.part + at * D + dd) = acc;
@@ -992,7 +992,7 @@ __global__ void __launch_bounds__(kWide < 8 ? 256 : 32 * kWide) paged_merge_kern
     for (int i = 0; i < kVec; i += 2)
         *reinterpret_cast<__nv_bfloat162 *>(out + i) = __floats2bfloat162_rn(acc[i] * inv, acc[i + 1] * inv);
     if (a.lse && lane == 0)
-        a.lse[row] = (mx - kWeightExp + log2f(sum)) * kLn2;
+        a.lse[row] = (mx + (log2f(sum) - kWeightExp)) * kLn2;
 }
 
 template <int D, int kWide>

@@ -1,0 +1,73 @@
+"""Decode attention over the paged 8-bit cache at the ends of the ranges that its header allows:
+scores of any finite size, value scales far apart, factors beyond fp32 on scores inside it."""
+import numpy as np
+import pytest
+import torch
+
+import invariant_deterministic_gemm_bi_b200 as bg
+from invariant_deterministic_gemm_bi_b200 import inputs
+from oracle import kv_cache as okv
+from tests.kv_util import DEV, assert_attention, attend, gaussian_codes, pool, queries
+
+pytestmark = pytest.mark.gpu
+ONE = 0x38   # e4m3 code of 1.0
+
+
+def sequence(n, heads, dim, page, seed, k_scale=1.0, v_scale=1.0):
+    """One sequence of n positions in the pages 0, 1, ...: zero keys, gaussian values."""
+    pages = -(-n // page)
+    k = pool(pages, page, heads, dim, fill=0)
+    v = gaussian_codes((pages, page, heads, dim), seed)
+    ks = torch.full((pages, heads), k_scale, device=DEV)
+    vs = torch.full((pages, heads), v_scale, device=DEV)
+    table = torch.arange(pages, dtype=torch.int32, device=DEV)[None].contiguous()
+    return bg.KvCache(k, v, ks, vs), table, torch.tensor([n], dtype=torch.int32, device=DEV)
+
+
+def oracle(cache, Q, table, lens, scale):
+    K, V = (okv.Cache(c.cpu().numpy(), s.cpu().numpy()).dequantised()
+            for c, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)))
+    return okv.paged_attention(inputs.to_numpy_bits(Q), K, V, table.cpu().numpy(), lens.tolist(), scale,
+                               v_scale=cache.v_scale.cpu().numpy())
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("top", [2.0 ** 23, 1.3 * 2.0 ** 24, 1.9 * 2.0 ** 24, 2.0 ** 25 + 8, 1.1 * 2.0 ** 27, 2.0 ** 30, 2.0 ** 100])
+def test_equal_scores_of_any_size(top, sign):
+    """Equal keys: the weights are 1 / n whatever the score, so the output is the mean value, off by 2^-8
+    of its own rounding and 2^-11 of the mean magnitude (fp16 weights; fp32 sums of at most 600 terms are
+    far below that), and the log-sum-exp is the score + log n, off by four fp32 roundings."""
+    for n in (1, 40, 600):
+        cache, table, lens = sequence(n, 2, 128, 32, seed=n)
+        cache.k.fill_(ONE)
+        Q = torch.ones((1, 8, 128), dtype=torch.bfloat16, device=DEV)
+        scale = sign * top / (128 * 1.4426950408889634)
+        O, lse = attend(cache, Q, table, lens, scale)
+        v = cache.v.view(torch.float8_e4m3fn).double().reshape(-1, 2, 128)[:n]
+        want, spread = v.mean(0), v.abs().mean(0)
+        got = O[0].double().view(2, 4, 128)
+        bound = 2.0 ** -8 * want.abs() + 2.0 ** -11 * (1 + 2.0 ** -8) * spread
+        assert torch.all((got - want[:, None]).abs() <= bound[:, None]), n
+        s = 128 * float(np.float32(scale))
+        assert torch.all((lse.double() - (s + np.log(n))).abs() <= 2.0 ** -22 * (abs(s) + np.log(n)) + 2.0 ** -20), n
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_large_scores_that_differ(dim):
+    """Scores 2^27 to 2^29 and thousands apart: the largest alone counts, its value comes out exactly."""
+    n = 700
+    cache, table, lens = sequence(n, 1, dim, 64, seed=5)
+    codes = torch.randint(1, 0x60, (n,), generator=inputs.generator(6, DEV), device=DEV).to(torch.uint8)
+    codes[codes == 0x5F] = 0x5E
+    at = torch.tensor([0, 31, 300, 699], device=DEV)
+    for best in at.tolist():
+        c = codes.clone()
+        c[best] = 0x5F
+        cache.k.view(-1, 1, dim)[:n, 0, 0] = c
+        Q = torch.zeros((1, 4, dim), dtype=torch.bfloat16, device=DEV)
+        Q[..., 0] = 2.0 ** 20
+        O, lse = attend(cache, Q, table, lens, 8.0)
+        v = cache.v.view(torch.float8_e4m3fn).view(-1, dim)[best].to(torch.bfloat16)
+        assert torch.equal(O[0], v.expand(4, -1)), best
+        s = 2.0 ** 23 * float(torch.tensor([0x5F], dtype=torch.uint8).view(torch.float8_e4m3fn).double())
+        assert torch.all((lse.double() - s).abs() <= 2.0 ** -22 * s)

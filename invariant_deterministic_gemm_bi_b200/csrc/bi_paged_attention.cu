@@ -35,8 +35,12 @@
 // Weights.  With sv the value scale of a position's page, the state's maximum M is that of
 // t_j = s_j log2 e + log2 sv, and the weight of a value's code is a_j = 2^(t_j - M + 15) <= 2^15,
 // rounded to fp16 (2^-11 of itself, a quarter of what bf16 would cost; the output is rounded to bf16
-// anyway); the softmax sum adds a_j / sv in fp32.  The value scale so costs nothing per element and
-// weights down to 2^-29 of the largest keep all of fp16's bits, whatever the scales.
+// anyway).  The value scale so costs nothing per element and weights down to 2^-29 of the largest keep
+// all of fp16's bits.  The softmax sum adds 2^(s_j log2 e - M) in fp32.  With scales from 2^-64 to 2^64
+// a position may count in it although t_j is far below M: by 128 for the scales and 54 for the score
+// (2^30 positions of 2^-54 are what an fp32 sum rounds away).  So a_j is held as 2^(t_j - M + 60), an
+// fp32 number down to t_j = M - 186, before it is rounded, and a change of M is applied in two halves.
+// The sum itself lies between 2^-64 and 2^94.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -72,7 +76,10 @@ constexpr int kItemRing = 4 * kItemBlock;   // entries of the items' table
 constexpr int kMaxBatch = 16384;            // sequences; an entry stands for several when there are more than entries
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kWeightExp = 15.0f;         // weights are held times 2^15
+constexpr float kWeightExp = 60.0f;         // weights are held times 2^60,
+constexpr float kToHalf = 0x1p-45f;         // times 2^15 in fp16,
+constexpr float kToSum = 0x1p-60f;          // and as they are, over their value scale, in the sum
+constexpr float kOutput = 0x1p-15f;         // takes the 2^15 out of the outputs
 // A wait that lasts this many SM cycles (two seconds) gives up; every later wait of the CTA then
 // returns at once and its outputs are NaN.
 constexpr uint64_t kWaitCycles = UINT64_C(4000000000);
@@ -203,6 +210,9 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi)
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
+// The square root of the factor that takes sums relative to the maximum `from` to the maximum `to`:
+// 2^(from - to) may be below fp32's range where a sum times it is not.
+__device__ __forceinline__ float half_factor(float from, float to) { return exp2_approx((from - to) * 0.5f); }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
 // s, or NaN unless 2^-64 <= s <= 2^64
@@ -244,7 +254,7 @@ struct Shared {
     uint8_t ring[kStages][kTiles][2][kMatrix];              // keys, values
     float state[kStates][kConsumers][MG][D];                // a chunk's outputs, not normalised
     uint4 q[2][NT][D / 32][32];                             // two items' queries, as the consumers' lanes hold them
-    float4 scale[kStages][kHalf / 16];                      // of 16 positions: key scale, log2 and 1 / of the value scale
+    float4 scale[kStages][kHalf / 16];                      // of 16 positions: key scale, log2 and kToSum / of the value scale
     Item items[kItemRing];
     Stage stage[kStages];
     float2 ml[kStates][kConsumers][kCols];                  // a chunk's maxima and sums
@@ -433,7 +443,7 @@ __device__ __forceinline__ void produce(Shared<D, MG> &sm, const AttnArgs &a, co
             if (mine) {
                 // approximate to 2^-22: a page's weights are all off by one factor below 2^-21
                 const float v = checked_scale(sc.v);
-                sm.scale[slot][group] = make_float4(checked_scale(sc.k), log2_approx(v), rcp_approx(v), 0.0f);
+                sm.scale[slot][group] = make_float4(checked_scale(sc.k), log2_approx(v), kToSum * rcp_approx(v), 0.0f);
             }
             if (s == min(1, stages - 1))
                 sc_next = scales_of(next, px_next);
@@ -576,7 +586,8 @@ __device__ __forceinline__ void consume(Shared<D, MG> &sm, const AttnArgs &a, in
                     mx[h] = fmaxf(mx[h], __shfl_xor_sync(kFull, mx[h], 8));
                     mx[h] = fmaxf(mx[h], __shfl_xor_sync(kFull, mx[h], 16));
                 }
-                const float corr[2] = {exp2_approx(m[n][0] - mx[0]), exp2_approx(m[n][1] - mx[1])};
+                const float half[2] = {half_factor(m[n][0], mx[0]), half_factor(m[n][1], mx[1])};
+                const float corr[2] = {half[0] * half[0], half[1] * half[1]};
                 float sum[2] = {0.0f, 0.0f};
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt) {
@@ -586,12 +597,12 @@ __device__ __forceinline__ void consume(Shared<D, MG> &sm, const AttnArgs &a, in
                         s[n][mt][x] = exp2_approx((s[n][mt][x] - mx[x & 1]) + kWeightExp);
                         sum[x & 1] = fmaf(s[n][mt][x], rsv[mt], sum[x & 1]);
                     }
-                    pf[n][mt][0] = transpose8x8(pack_half(s[n][mt][0], s[n][mt][1]));
-                    pf[n][mt][1] = transpose8x8(pack_half(s[n][mt][2], s[n][mt][3]));
+                    pf[n][mt][0] = transpose8x8(pack_half(s[n][mt][0] * kToHalf, s[n][mt][1] * kToHalf));
+                    pf[n][mt][1] = transpose8x8(pack_half(s[n][mt][2] * kToHalf, s[n][mt][3] * kToHalf));
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    l[n][h] = fmaf(l[n][h], corr[h], sum[h]);
+                    l[n][h] = fmaf(l[n][h] * half[h], half[h], sum[h]);
                     m[n][h] = mx[h];
                 }
                 // outputs so far to the new maximum
@@ -728,8 +739,8 @@ __device__ __forceinline__ void add_states(Shared<D, MG> &sm, const AttnArgs &a,
 #pragma unroll
         for (int w = 0; w < kConsumers; ++w) {
             const float4 v = *reinterpret_cast<const float4 *>(&sm.state[buf][w][0][0] + state_offset<D>(head, dd));
-            const float f = exp2_approx(ml[w].x - mx);
-            sum = fmaf(ml[w].y, f, sum);
+            const float half = half_factor(ml[w].x, mx), f = half * half;
+            sum = fmaf(ml[w].y * half, half, sum);
             acc.x = fmaf(v.x, f, acc.x);
             acc.y = fmaf(v.y, f, acc.y);
             acc.z = fmaf(v.z, f, acc.z);
@@ -739,13 +750,13 @@ __device__ __forceinline__ void add_states(Shared<D, MG> &sm, const AttnArgs &a,
         const int64_t row = static_cast<int64_t>(it.b) * a.hq + h;
         const bool dead = *static_cast<volatile int *>(&sm.dead) != 0;
         if (it.chunks == 1) {
-            const float r = dead ? NAN : 1.0f / sum;
+            const float r = dead ? NAN : kOutput / sum;
             uint2 y;
             *reinterpret_cast<__nv_bfloat162 *>(&y.x) = __floats2bfloat162_rn(acc.x * r, acc.y * r);
             *reinterpret_cast<__nv_bfloat162 *>(&y.y) = __floats2bfloat162_rn(acc.z * r, acc.w * r);
             *reinterpret_cast<uint2 *>(a.out + it.b * a.ldo + static_cast<int64_t>(h) * D + dd) = y;
             if (a.lse && dd == 0)
-                a.lse[row] = dead ? NAN : (mx + (log2f(sum) - kWeightExp)) * kLn2;
+                a.lse[row] = dead ? NAN : (mx + log2f(sum)) * kLn2;
         } else {
             const int64_t at = row * a.chunks + it.chunk;
             *reinterpret_cast<float4 *>(a.part + at * D + dd) = acc;
@@ -958,8 +969,8 @@ __global__ void __launch_bounds__(kWide < 8 ? 256 : 32 * kWide) paged_merge_kern
 #pragma unroll
         for (int j = 0; j < kEight; ++j) {
             // a chunk of NaN scores has no maximum: its sum is NaN and stays so
-            const float f = exp2_approx(x[j].x - (mx == -INFINITY ? 0.0f : mx));
-            sum = fmaf(x[j].y, f, sum);
+            const float half = half_factor(x[j].x, mx == -INFINITY ? 0.0f : mx), f = half * half;
+            sum = fmaf(x[j].y * half, half, sum);
 #pragma unroll
             for (int i = 0; i < kVec; ++i)
                 acc[i] = fmaf(v[j][i], f, acc[i]);
@@ -980,19 +991,19 @@ __global__ void __launch_bounds__(kWide < 8 ? 256 : 32 * kWide) paged_merge_kern
     for (int e = 0; e < eights; ++e)
         mx = fmaxf(mx, ml_s[r][e].x);
     for (int e = 0; e < eights; ++e) {
-        const float f = exp2_approx(ml_s[r][e].x - (mx == -INFINITY ? 0.0f : mx));
-        sum = fmaf(ml_s[r][e].y, f, sum);
+        const float half = half_factor(ml_s[r][e].x, mx == -INFINITY ? 0.0f : mx), f = half * half;
+        sum = fmaf(ml_s[r][e].y * half, half, sum);
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
             acc[i] = fmaf(acc_s[r][e][lane * kVec + i], f, acc[i]);
     }
-    const float inv = 1.0f / sum;
+    const float inv = kOutput / sum;
     __nv_bfloat16 *out = a.out + b * a.ldo + (row - static_cast<int64_t>(b) * a.hq) * D + lane * kVec;
 #pragma unroll
     for (int i = 0; i < kVec; i += 2)
         *reinterpret_cast<__nv_bfloat162 *>(out + i) = __floats2bfloat162_rn(acc[i] * inv, acc[i + 1] * inv);
     if (a.lse && lane == 0)
-        a.lse[row] = (mx + (log2f(sum) - kWeightExp)) * kLn2;
+        a.lse[row] = (mx + log2f(sum)) * kLn2;
 }
 
 template <int D, int kWide>

@@ -71,3 +71,44 @@ def test_large_scores_that_differ(dim):
         assert torch.equal(O[0], v.expand(4, -1)), best
         s = 2.0 ** 23 * float(torch.tensor([0x5F], dtype=torch.uint8).view(torch.float8_e4m3fn).double())
         assert torch.all((lse.double() - s).abs() <= 2.0 ** -22 * s)
+
+
+def log2_keys(cache, rows, x):
+    """Keys whose score is x in base 2 for a query of ones in dimension 0 and scale 2 ln 2: x / 2 in dimension 0."""
+    code = torch.tensor([x / 2], dtype=torch.float32).to(torch.float8_e4m3fn).view(torch.uint8)
+    assert float(code.view(torch.float8_e4m3fn).float()) == x / 2
+    cache.k.view(-1, cache.num_heads, cache.head_dim)[rows, :, 0] = code.to(DEV)
+
+
+# (positions, page, head_dim, pages in the large scale, base-2 score of the others below theirs)
+FAR = [(17, 16, 64, [1], -14), (17, 16, 128, [1], -14), (256, 32, 128, [0], 0), (256, 32, 64, [5], -8),
+       (256, 32, 128, [7], -16), (2000, 64, 64, [0], 0), (2000, 64, 128, [31], -4), (9000, 256, 64, [17], -8),
+       (131072 + 256, 256, 64, [0], -14), (131072 + 256, 256, 64, [512], -14), (20000, 16, 128, [3, 700], -20)]
+
+
+@pytest.mark.parametrize("n,page,dim,large,below", FAR)
+@pytest.mark.parametrize("far", [64, 63.5])
+def test_value_scales_at_both_ends_of_their_range(n, page, dim, large, below, far):
+    # positions of a small value scale add nothing to the output, but all of them to the softmax sum
+    cache, table, lens = sequence(n, 1, dim, page, seed=11, v_scale=2.0 ** -far)
+    log2_keys(cache, slice(None), below)
+    for p in large:
+        cache.v_scale[p] = 2.0 ** far
+        cache.k[p] = 0
+    Q = torch.zeros((1, 4, dim), dtype=torch.bfloat16, device=DEV)
+    Q[..., 0] = 1
+    scale = 2 * np.log(2.0)
+    O, lse = attend(cache, Q, table, lens, scale)
+    assert_attention(O, lse, oracle(cache, Q, table, lens, scale), scale, dim)
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_value_scales_over_all_of_their_range(seed):
+    g = inputs.generator(100 + seed, DEV)
+    for n, page, dim, heads in ((77, 16, 64, 2), (700, 16, 128, 1), (5000, 32, 64, 1), (30000, 64, 128, 1)):
+        cache, table, lens = sequence(n, heads, dim, page, seed=12 + seed)
+        cache.k.copy_(gaussian_codes(cache.k.shape, 13 + seed))
+        cache.v_scale.copy_(torch.exp2(torch.randint(-64, 65, cache.v_scale.shape, generator=g, device=DEV).float()))
+        Q = queries(1, 4 * heads, dim, 14 + seed, std=3.0)
+        O, lse = attend(cache, Q, table, lens, 0.3)
+        assert_attention(O, lse, oracle(cache, Q, table, lens, 0.3), 0.3, dim)

@@ -47,8 +47,8 @@ size_t bi_paged_decode_attention_workspace_bytes(int64_t B, int Hq, int D, int64
  *   output will do); O [B][ldo] bf16; lse fp32 [B][Hq] or NULL;
  *   block_table int32 [B][ld_table], ld_table >= max_pages; seq_lens int32 [B].
  * scale: any finite value.  window: 0, or the number of positions a query sees.
- * Hq a multiple of num_heads, at most 16 query heads per key/value head.  Q finite; products
- * of Q and K beyond the fp32 range give NaN.
+ * Hq a multiple of num_heads, at most 16 query heads per key/value head.  Q finite.  Where s_j log2 e
+ * itself is beyond the fp32 range, the query head's outputs are NaN or those without position j.
  * workspace: at least bi_paged_decode_attention_workspace_bytes(B, Hq, head_dim, max_pages *
  * page_size) bytes, 16-byte aligned (NULL when that is 0).  The call overwrites it; calls that may
  * run at the same time need workspaces of their own.

@@ -76,6 +76,8 @@ constexpr int kItemRing = 4 * kItemBlock;   // entries of the items' table
 constexpr int kMaxBatch = 16384;            // sequences; an entry stands for several when there are more than entries
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+// A head's factor up to which products with every valid key scale stay in fp32's range.
+constexpr float kPlainFactor = 0x1p62f;
 constexpr float kWeightExp = 60.0f;         // weights are held times 2^60,
 constexpr float kToHalf = 0x1p-45f;         // times 2^15 in fp16,
 constexpr float kToSum = 0x1p-60f;          // and as they are, over their value scale, in the sum
@@ -106,7 +108,8 @@ struct AttnArgs {
     float2 *part_ml;    // [b][hq][chunks] (M, sum)
     int64_t ldq, ldo, ld_table, window;
     int num_pages, max_len, b, hq, heads, group, page_shift, chunks;
-    float scale;
+    float scale_m;      // scale * log2 e = scale_m * 2^scale_e
+    int scale_e;
 };
 
 // What of a sequence is attended: positions [lo, hi), in steps from `first`.  A sequence without any,
@@ -258,7 +261,8 @@ struct Shared {
     Item items[kItemRing];
     Stage stage[kStages];
     float2 ml[kStates][kConsumers][kCols];                  // a chunk's maxima and sums
-    float qc[2][kCols];                                     // scale * log2 e * the power of two taken out
+    float qc[2][kCols];                                     // scale * log2 e * the power of two taken out,
+    int qe[2][kCols];                                       // and the exponent e of it as scale_m * 2^e
     uint64_t full[kStages], empty[kStages];                 // a stage is filled, is consumed
     // An item's states are written; the helpers are done with the item two before: its states are read,
     // and the queries that take the place of its own are there.  Even and odd items apart, since
@@ -480,6 +484,7 @@ __device__ __forceinline__ void consume(Shared<D, MG> &sm, const AttnArgs &a, in
     float qc[NT][2];                  // factors of heads 2t, 2t + 1
     float o[NT][D / 16][4];           // [dimension 16 j + 2 g, + 1][head 2t, 2t + 1]
     float m[NT][2], l[NT][2];
+    bool plain = true;                // every head's factor is below kPlainFactor
     int slot = warp / kTiles;         // stages of this warp's half of the steps
     uint32_t parity = 0;
     int item = 0;
@@ -510,6 +515,11 @@ __device__ __forceinline__ void consume(Shared<D, MG> &sm, const AttnArgs &a, in
                 m[n][0] = m[n][1] = -INFINITY;
                 l[n][0] = l[n][1] = 0.0f;
             }
+            plain = true;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                plain = plain && fabsf(qc[n][0]) < kPlainFactor && fabsf(qc[n][1]) < kPlainFactor;
+            plain = __all_sync(kFull, plain);
         }
         const int key0 = st.key0 + tile * kTile;
         if (key0 < st.hi && key0 + kTile > st.lo) {
@@ -558,12 +568,23 @@ __device__ __forceinline__ void consume(Shared<D, MG> &sm, const AttnArgs &a, in
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 float mx[2] = {m[n][0], m[n][1]};
+                if (plain) {
 #pragma unroll
-                for (int mt = 0; mt < 2; ++mt) {
-                    const float c[2] = {qc[n][0] * sk[mt], qc[n][1] * sk[mt]};
+                    for (int mt = 0; mt < 2; ++mt) {
+                        const float c[2] = {qc[n][0] * sk[mt], qc[n][1] * sk[mt]};
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        s[n][mt][x] = fmaf(s[n][mt][x], c[x & 1], lsv[mt]);
+                        for (int x = 0; x < 4; ++x)
+                            s[n][mt][x] = fmaf(s[n][mt][x], c[x & 1], lsv[mt]);
+                    }
+                } else {   // rare: the factor may be beyond fp32 where a score is not, so its power of two comes in two halves
+                    const int *e = &sm.qe[item & 1][n * 8 + 2 * t];
+                    const float p[2][2] = {{pow2(max(e[0] >> 1, -126)), pow2(max(e[0] - (e[0] >> 1), -126))},
+                                           {pow2(max(e[1] >> 1, -126)), pow2(max(e[1] - (e[1] >> 1), -126))}};
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            s[n][mt][x] = s[n][mt][x] * (a.scale_m * sk[mt]) * p[x & 1][0] * p[x & 1][1] + lsv[mt];
                 }
                 if (!whole) {
 #pragma unroll
@@ -675,7 +696,7 @@ template <int D, int MG>
 struct Queries {
     static constexpr int kHeads = (MG + kHelpers - 1) / kHelpers;
     uint2 x[kHeads];
-    float c[kHeads];
+    int e[kHeads];       // the query's factor is scale_m * 2^e
 
     __device__ __forceinline__ void load(const AttnArgs &a, const Item &it, int w)
     {
@@ -696,11 +717,11 @@ struct Queries {
             uint32_t top = max(max(x[i].x & 0x7fffu, (x[i].x >> 16) & 0x7fffu), max(x[i].y & 0x7fffu, (x[i].y >> 16) & 0x7fffu));
             top = __reduce_max_sync(kFull, top);
             // the largest magnitude goes to [2^14, 2^15)
-            const int e = top == 0 ? 0 : max(-120, static_cast<int>(top >> 7) - 127 - 14);
-            const float down = pow2(-e);
+            const int out = top == 0 ? 0 : max(-120, static_cast<int>(top >> 7) - 127 - 14);
+            const float down = pow2(-out);
             x[i] = make_uint2(pack_half(__uint_as_float(x[i].x << 16) * down, __uint_as_float(x[i].x & 0xffff0000u) * down),
                               pack_half(__uint_as_float(x[i].y << 16) * down, __uint_as_float(x[i].y & 0xffff0000u) * down));
-            c[i] = a.scale * kLog2e * pow2(e);
+            e[i] = a.scale_e + out;
         }
     }
     __device__ __forceinline__ void store(Shared<D, MG> &sm, const AttnArgs &a, int buf, int w) const
@@ -712,8 +733,10 @@ struct Queries {
             if (head < a.group) {
                 if (lane < D / 4)   // as the consumers' lanes hold them
                     reinterpret_cast<uint2 *>(&sm.q[buf][head >> 3][ks >> 1][(head & 7) * 4 + (lane & 3)])[ks & 1] = x[i];
-                if (lane == 0)
-                    sm.qc[buf][head] = c[i];
+                if (lane == 0) {   // below 2^-126 it makes scores of at most 2^-31 either way
+                    sm.qc[buf][head] = a.scale_m * pow2(max(-126, min(127, e[i])));
+                    sm.qe[buf][head] = e[i];
+                }
             }
         }
     }
@@ -852,8 +875,10 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_c
     // query columns that no head fills stay zero
     for (int x = tid; x < 2 * S::NT * (D / 32) * 32; x += kThreads)
         (&sm.q[0][0][0][0])[x] = make_uint4(0, 0, 0, 0);
-    if (tid < 2 * S::kCols)
+    if (tid < 2 * S::kCols) {
         (&sm.qc[0][0])[tid] = 0.0f;
+        (&sm.qe[0][0])[tid] = 0;
+    }
     bi_kv::dependency_wait();
 
     // chunks before each entry, class by class, one entry a thread
@@ -1134,7 +1159,7 @@ bi_status_t bi_paged_decode_attention(const bi_kv_cache_t *cache, const void *Q,
     a.group = Hq / cache->num_heads;
     a.page_shift = bi_kv::log2_of(cache->page_size);
     a.chunks = static_cast<int>(most_chunks(max_len));
-    a.scale = scale;
+    a.scale_m = std::frexp(scale, &a.scale_e) * kLog2e;
     a.part = static_cast<float *>(workspace);
     a.part_ml = reinterpret_cast<float2 *>(a.part + B * Hq * a.chunks * cache->head_dim);
     CUtensorMap k_map, v_map;

@@ -112,3 +112,35 @@ def test_value_scales_over_all_of_their_range(seed):
         Q = queries(1, 4 * heads, dim, 14 + seed, std=3.0)
         O, lse = attend(cache, Q, table, lens, 0.3)
         assert_attention(O, lse, oracle(cache, Q, table, lens, 0.3), 0.3, dim)
+
+
+@pytest.mark.parametrize("scale,std", [(3e38, 1.0), (-3e38, 30.0), (2.4e38, 1e-3), (1e30, 1e30), (1e38, 1e38)])
+def test_zero_keys_have_score_zero_whatever_the_factors(scale, std):
+    cache, table, lens = sequence(300, 2, 128, 32, seed=21, k_scale=2.0 ** -64)
+    cache.k_scale[3:5] = 2.0 ** 64
+    Q = queries(1, 8, 128, 22, std=std)
+    O, lse = attend(cache, Q, table, lens, scale)
+    assert_attention(O, lse, oracle(cache, Q, table, lens, scale), 0.0, 128)
+
+
+@pytest.mark.parametrize("scale,q,k_scale", [(3e38, 2.0 ** 20, 2.0 ** -64), (2.4e38, 1.0, 2.0 ** -40), (1e30, 2.0 ** 60, 2.0 ** -64),
+                                             (1e25, 2.0 ** 80, 2.0 ** -60), (-3e38, 2.0 ** 30, 2.0 ** -64)])
+def test_scores_inside_fp32_of_factors_beyond_it(scale, q, k_scale):
+    """scale * log2 e * |q| is beyond fp32 or near its end, the scores are not: distinct keys, the largest
+    score alone counts."""
+    n = 200
+    cache, table, lens = sequence(n, 1, 64, 16, seed=23, k_scale=k_scale)
+    rows = cache.k.view(-1, 1, 64)
+    rows[:n, 0, 0] = torch.randint(8, 40, (n,), generator=inputs.generator(24, DEV), device=DEV).to(torch.uint8)
+    for best in (0, 17, 133, 199):
+        codes = rows[:n, 0, 0].clone()
+        rows[best, 0, 0] = 48 if scale > 0 else 4
+        Q = torch.zeros((1, 2, 64), dtype=torch.bfloat16, device=DEV)
+        Q[..., 0], Q[0, 1, 5] = q, 1e-3
+        s = float(np.float32(scale)) * q * k_scale * float(rows[best:best + 1, 0, 0].view(torch.float8_e4m3fn).double())
+        assert abs(s) * 1.5 < 3e38
+        O, lse = attend(cache, Q, table, lens, scale)
+        v = cache.v.view(torch.float8_e4m3fn).view(-1, 64)[best].to(torch.bfloat16)
+        assert torch.equal(O[0], v.expand(2, -1)), best
+        assert torch.all((lse.double() - s).abs() <= 2.0 ** -21 * abs(s))
+        rows[:n, 0, 0] = codes

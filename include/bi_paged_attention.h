@@ -38,7 +38,8 @@ extern "C" {
 
 /* Bytes of workspace bi_paged_decode_attention needs for B sequences of up to max_len positions
  * (max_pages * page_size): one partial result per chunk, query head and sequence.  0 when no
- * sequence can have two chunks, or for sizes below 1. */
+ * sequence can have two chunks, and for sizes that the call refuses: below 1, B above 16384, B * Hq
+ * from 2^31, D other than 64 and 128, max_len above 2^30. */
 size_t bi_paged_decode_attention_workspace_bytes(int64_t B, int Hq, int D, int64_t max_len);
 
 /*

@@ -74,6 +74,7 @@ constexpr int kClasses = 4;                 // of chunks, by steps: 4 and more, 
 constexpr int kItemBlock = 32;              // items whose table entries one warp makes at once
 constexpr int kItemRing = 4 * kItemBlock;   // entries of the items' table
 constexpr int kMaxBatch = 16384;            // sequences; an entry stands for several when there are more than entries
+constexpr int64_t kMaxLen = INT64_C(1) << 30;   // positions of a sequence
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // A head's factor up to which products with every valid key scale stay in fp32's range.
@@ -1096,8 +1097,8 @@ extern "C" {
 
 size_t bi_paged_decode_attention_workspace_bytes(int64_t B, int Hq, int D, int64_t max_len)
 {
-    if (B < 1 || Hq < 1 || D < 1 || max_len < 1)
-        return 0;
+    if (B < 1 || Hq < 1 || max_len < 1 || B > kMaxBatch || B * Hq > INT32_MAX || (D != 64 && D != 128) || max_len > kMaxLen)
+        return 0;   // the call refuses these, and the sizes below would not fit their types
     const int64_t chunks = most_chunks(max_len);
     return chunks == 1 ? 0 : static_cast<size_t>(B) * Hq * chunks * (D + 2) * sizeof(float);
 }
@@ -1127,7 +1128,7 @@ bi_status_t bi_paged_decode_attention(const bi_kv_cache_t *cache, const void *Q,
         !bi_kv::aligned(seq_lens, 4) || !bi_kv::aligned(lse, 4))
         return BI_ERR_ALIGNMENT;
     const int64_t max_len = max_pages * cache->page_size;
-    if (max_len > (INT64_C(1) << 30) || B * cache->num_heads > (INT64_C(1) << 30) / most_chunks(max_len))
+    if (max_len > kMaxLen || B * cache->num_heads > (INT64_C(1) << 30) / most_chunks(max_len))
         return BI_ERR_UNSUPPORTED_SHAPE;
     const size_t need = bi_paged_decode_attention_workspace_bytes(B, Hq, cache->head_dim, max_len);
     if (need > 0) {

@@ -90,6 +90,20 @@ def test_attention_checks_its_workspace():
         assert bg.bi_paged_decode_attention_workspace_bytes(*sizes) == 0
 
 
+@pytest.mark.parametrize("sizes", [(1, 8, 128, 2 ** 30 + 1), (1, 8, 128, 2 ** 38 + 1), (1, 8, 64, 2 ** 39 + 1),
+                                   (1, 8, 128, 2 ** 62), (1, 8, 128, 2 ** 63 - 1), (16385, 8, 128, 4096),
+                                   (2 ** 62, 8, 128, 4096), (16384, 2 ** 17, 128, 4096), (1, 8, 96, 4096),
+                                   (1, 8, 2 ** 31 - 1, 4096)])
+def test_workspace_sizes_beyond_the_limits_are_zero(sizes):
+    # max_len from 2^38 on once did not return, from 2^30 on the number was of a truncated length
+    assert bg.bi_paged_decode_attention_workspace_bytes(*sizes) == 0
+
+
+def test_the_largest_workspace_sizes():
+    assert bg.bi_paged_decode_attention_workspace_bytes(1, 8, 128, 2 ** 30) == 8 * 128 * 130 * 4
+    assert bg.bi_paged_decode_attention_workspace_bytes(16384, 2 ** 17 - 1, 64, 2 ** 30) == 16384 * (2 ** 17 - 1) * 128 * 66 * 4
+
+
 def test_accepted_arguments_reach_the_device_probe():
     if torch.cuda.is_available():
         pytest.skip("the pointers are made up")

@@ -66,6 +66,23 @@ bi_status_t bi_paged_decode_attention(const bi_kv_cache_t *cache, const void *Q,
                                       size_t workspace_bytes, void *O, int64_t ldo, float *lse,
                                       cudaStream_t stream);
 
+/*
+ * The time limit, in nanoseconds, of every wait inside the attention kernels that this process launches
+ * from now on (default 2e9, i.e. 2 s; 0 restores the default), counted as by bi_gemm_set_wait_timeout;
+ * a captured call keeps the limit it was captured with.  A thread block whose wait runs out waits for
+ * its copies in flight and ends: what it has not finished by then is NaN in O and lse, nothing is left
+ * as it was, the other blocks' outputs are right and the context stays usable.  No status word
+ * reports it.
+ */
+bi_status_t bi_paged_decode_attention_set_wait_timeout(uint64_t timeout_ns);
+
+/*
+ * Test-only fault injection on the host side of the launch, for the whole process: every thread block
+ * leaves its n-th load out (counted from 1; 0: none), so that a wait for it must end by its time
+ * limit.  Never set in production.
+ */
+bi_status_t bi_paged_decode_attention_debug_skip_load(uint32_t n);
+
 #ifdef __cplusplus
 }
 #endif

@@ -54,6 +54,8 @@ from .binding import (  # noqa: F401
     bi_moe_gather_rows,
     bi_moe_route_topk,
     bi_paged_decode_attention,
+    bi_paged_decode_attention_debug_skip_load,
+    bi_paged_decode_attention_set_wait_timeout,
     bi_paged_decode_attention_workspace_bytes,
     bi_quantize_e2m1,
     bi_status_string,

@@ -45,6 +45,7 @@ EXPORTED = [
     "bi_quantize_e2m1",
     "bi_kv_block_tables", "bi_kv_append_e4m3",
     "bi_paged_decode_attention", "bi_paged_decode_attention_workspace_bytes",
+    "bi_paged_decode_attention_set_wait_timeout", "bi_paged_decode_attention_debug_skip_load",
 ]
 
 
@@ -175,6 +176,10 @@ def load_library(path: str = LIB_PATH):
     lib.bi_paged_decode_attention.restype = i32
     lib.bi_paged_decode_attention.argtypes = [pc, vp, i64, vp, i64, i64, vp, i64, i32, ctypes.c_float,
                                               i64, vp, ctypes.c_size_t, vp, i64, vp, vp]
+    lib.bi_paged_decode_attention_set_wait_timeout.restype = i32
+    lib.bi_paged_decode_attention_set_wait_timeout.argtypes = [u64]
+    lib.bi_paged_decode_attention_debug_skip_load.restype = i32
+    lib.bi_paged_decode_attention_debug_skip_load.argtypes = [u32]
     if path == LIB_PATH:
         _LIB = lib
     return lib
@@ -664,3 +669,14 @@ def bi_paged_decode_attention(cache: KvCache, Q, block_table, seq_lens, O, scale
         window, _ptr(workspace), nbytes, O.data_ptr(), ldo, _ptr(lse), _stream_on(torch, device, stream)),
         "bi_paged_decode_attention")
     return O
+
+
+def bi_paged_decode_attention_set_wait_timeout(timeout_ns: int):
+    """Limit of every wait inside the attention kernels launched from now on (0: the default, 2 s)."""
+    _check(load_library().bi_paged_decode_attention_set_wait_timeout(timeout_ns),
+           "bi_paged_decode_attention_set_wait_timeout")
+
+
+def bi_paged_decode_attention_debug_skip_load(n: int):
+    """Test only: every thread block leaves its n-th load out (0: none)."""
+    _check(load_library().bi_paged_decode_attention_debug_skip_load(n), "bi_paged_decode_attention_debug_skip_load")

@@ -46,6 +46,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -83,9 +84,7 @@ constexpr float kWeightExp = 60.0f;         // weights are held times 2^60,
 constexpr float kToHalf = 0x1p-45f;         // times 2^15 in fp16,
 constexpr float kToSum = 0x1p-60f;          // and as they are, over their value scale, in the sum
 constexpr float kOutput = 0x1p-15f;         // takes the 2^15 out of the outputs
-// A wait that lasts this many SM cycles (two seconds) gives up; every later wait of the CTA then
-// returns at once and its outputs are NaN.
-constexpr uint64_t kWaitCycles = UINT64_C(4000000000);
+constexpr uint64_t kWaitNs = UINT64_C(2000000000);   // limit of a wait, unless the program sets another
 static_assert(kStep == 2 * kHalf, "a step is two stages");
 
 // Steps per chunk of a sequence of `steps` steps.  Opening and closing a chunk costs about as much as
@@ -111,6 +110,8 @@ struct AttnArgs {
     int num_pages, max_len, b, hq, heads, group, page_shift, chunks;
     float scale_m;      // scale * log2 e = scale_m * 2^scale_e
     int scale_e;
+    uint32_t skip_load;   // test only: the stage, counted from 1, that producers leave out
+    uint64_t wait_cycles;
 };
 
 // What of a sequence is attended: positions [lo, hi), in steps from `first`.  A sequence without any,
@@ -292,11 +293,16 @@ __device__ __forceinline__ int state_offset(int head, int d)
     return head * D + (d ^ (((head >> 1) & 3) << 3));
 }
 
+// Whether the phase completed, one answer for the whole warp.  After a wait that gave up no warp goes on
+// as if it had not: it neither reads, writes, copies nor arrives, so every other warp that needs it
+// gives up at once, and what is running keeps its order.
 template <typename S>
-__device__ __forceinline__ void wait_for(S &sm, uint64_t *bar, uint32_t parity)
+__device__ __forceinline__ bool wait_for(S &sm, const AttnArgs &a, uint64_t *bar, uint32_t parity)
 {
-    if (!bi::ptx::mbar_wait(bar, parity, kWaitCycles, &sm.dead))
-        *static_cast<volatile int *>(&sm.dead) = 1;
+    if (__all_sync(kFull, bi::ptx::mbar_wait(bar, parity, a.wait_cycles, &sm.dead)))
+        return true;
+    *static_cast<volatile int *>(&sm.dead) = 1;
+    return false;
 }
 
 // One arrival of this warp, which releases what all of it has written.
@@ -403,9 +409,13 @@ __device__ __forceinline__ void produce(Shared<D, MG> &sm, const AttnArgs &a, co
     int slot = 0;
     uint32_t parity = 1;     // of a stage not used yet
     bool used_all = false;   // every stage has been used
-    auto take_slot = [&]() { wait_for(sm, &sm.empty[slot], parity); };
+    bool ok = true;          // no wait has given up
+    uint32_t skip = a.skip_load;   // 1: the next stage is left out
+    auto take_slot = [&]() { return ok = wait_for(sm, a, &sm.empty[slot], parity); };
     auto give_slot = [&]() {
-        warp_arrive(&sm.full[slot]);   // releases the words stored for it
+        if (skip != 1)
+            warp_arrive(&sm.full[slot]);   // releases the words stored for it
+        skip -= skip != 0;
         if (++slot == S::kStages) {
             slot = 0;
             parity ^= 1;
@@ -417,7 +427,7 @@ __device__ __forceinline__ void produce(Shared<D, MG> &sm, const AttnArgs &a, co
     Item it = sm.items[0];
     Pages px = pages_of(it, 0);
     Scales sc = scales_of(it, px);
-    while (it.b >= 0 && !*static_cast<volatile int *>(&sm.dead)) {
+    while (ok && it.b >= 0) {
         const int stages = min(kBlock, 2 * it.steps - block * kBlock);
         // the next block, of this item or of the next one
         int next_block = block + 1;
@@ -428,10 +438,9 @@ __device__ __forceinline__ void produce(Shared<D, MG> &sm, const AttnArgs &a, co
         }
         Pages px_next = pages_of(next, next_block);
         Scales sc_next = {1.0f, 1.0f};
-        for (int s = 0; s < stages; ++s) {
-            take_slot();
+        for (int s = 0; s < stages && take_slot(); ++s) {
             const bool mine = quarter == s;
-            const bool issue = mine && px.ok && (group * 16 & (box - 1)) == 0;
+            const bool issue = mine && px.ok && (group * 16 & (box - 1)) == 0 && skip != 1;
             const uint32_t boxes = __popc(__ballot_sync(kFull, issue));
             if (lane == 0) {
                 const int at = block * kBlock + s;
@@ -459,18 +468,18 @@ __device__ __forceinline__ void produce(Shared<D, MG> &sm, const AttnArgs &a, co
         px = px_next;
         sc = sc_next;
     }
-    for (int half = 0; half < 2; ++half) {   // both halves of the consumers are told
-        take_slot();
-        if (lane == 0)
-            sm.stage[slot] = {0, 0, 0, kEnd};
-        give_slot();
-    }
-    // Consumers wait for every stage, unless a wait has given up: then copies may be in flight still.
-    // The last use of a stage before `slot` was in this round of the ring, of the others in the round before.
-    if (*static_cast<volatile int *>(&sm.dead))
-        for (int i = 0; i < S::kStages; ++i)
-            if (i < slot || used_all)
-                bi::ptx::mbar_wait(&sm.full[i], i < slot ? parity ^ 1 : parity, kWaitCycles, nullptr);
+    for (int half = 0; ok && half < 2; ++half)   // both halves of the consumers are told
+        if (take_slot()) {
+            if (lane == 0)
+                sm.stage[slot] = {0, 0, 0, kEnd};
+            give_slot();
+        }
+    // No copy is in flight when the block ends, whoever has given up: consumers that go on have waited for
+    // every stage themselves.  The last use of a stage before `slot` was in this round of the ring, of the
+    // others in the round before.
+    for (int i = 0; i < S::kStages; ++i)
+        if (i < slot || used_all)
+            bi::ptx::mbar_wait(&sm.full[i], i < slot ? parity ^ 1 : parity, a.wait_cycles, nullptr);
 }
 
 template <int D, int MG>
@@ -490,12 +499,14 @@ __device__ __forceinline__ void consume(Shared<D, MG> &sm, const AttnArgs &a, in
     uint32_t parity = 0;
     int item = 0;
     while (true) {
-        wait_for(sm, &sm.full[slot], parity);
+        if (!wait_for(sm, a, &sm.full[slot], parity))
+            break;
         const Stage st = sm.stage[slot];
-        if ((st.flags & kEnd) || *static_cast<volatile int *>(&sm.dead))
+        if (st.flags & kEnd)
             break;
         if (st.flags & kFirst) {
-            wait_for(sm, &sm.helped[item & 1], (item >> 1) & 1);
+            if (!wait_for(sm, a, &sm.helped[item & 1], (item >> 1) & 1))
+                break;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -667,7 +678,8 @@ __device__ __forceinline__ void consume(Shared<D, MG> &sm, const AttnArgs &a, in
             const int buf = S::kStates == 1 ? 0 : item & 1;
             ++item;
             if constexpr (S::kStates == 1)
-                wait_for(sm, &sm.helped[item & 1], (item >> 1) & 1);   // the states of the item before have been read
+                if (!wait_for(sm, a, &sm.helped[item & 1], (item >> 1) & 1))   // the states of the item before have been read
+                    break;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -743,7 +755,30 @@ struct Queries {
     }
 };
 
-// The eight states of an item added in warp order, and the result or the chunk's part stored.
+// Four dimensions of a query head of an item: its result, or its chunk's part, from the maximum, the sum
+// and the outputs that belong to them.
+template <int D>
+__device__ __forceinline__ void put(const AttnArgs &a, const Item &it, int head, int dd, float mx, float sum, const float4 &acc)
+{
+    const int h = it.kvh * a.group + head;
+    const int64_t row = static_cast<int64_t>(it.b) * a.hq + h;
+    if (it.chunks == 1) {
+        const float r = kOutput / sum;
+        uint2 y;
+        *reinterpret_cast<__nv_bfloat162 *>(&y.x) = __floats2bfloat162_rn(acc.x * r, acc.y * r);
+        *reinterpret_cast<__nv_bfloat162 *>(&y.y) = __floats2bfloat162_rn(acc.z * r, acc.w * r);
+        *reinterpret_cast<uint2 *>(a.out + it.b * a.ldo + static_cast<int64_t>(h) * D + dd) = y;
+        if (a.lse && dd == 0)
+            a.lse[row] = (mx + log2f(sum)) * kLn2;
+    } else {
+        const int64_t at = row * a.chunks + it.chunk;
+        *reinterpret_cast<float4 *>(a.part + at * D + dd) = acc;
+        if (dd == 0)
+            a.part_ml[at] = make_float2(mx, sum);
+    }
+}
+
+// The eight states of an item added in warp order.
 template <int D, int MG>
 __device__ __forceinline__ void add_states(Shared<D, MG> &sm, const AttnArgs &a, const Item &it, int buf, int tid)
 {
@@ -770,22 +805,28 @@ __device__ __forceinline__ void add_states(Shared<D, MG> &sm, const AttnArgs &a,
             acc.z = fmaf(v.z, f, acc.z);
             acc.w = fmaf(v.w, f, acc.w);
         }
-        const int h = it.kvh * a.group + head;
-        const int64_t row = static_cast<int64_t>(it.b) * a.hq + h;
-        const bool dead = *static_cast<volatile int *>(&sm.dead) != 0;
-        if (it.chunks == 1) {
-            const float r = dead ? NAN : kOutput / sum;
-            uint2 y;
-            *reinterpret_cast<__nv_bfloat162 *>(&y.x) = __floats2bfloat162_rn(acc.x * r, acc.y * r);
-            *reinterpret_cast<__nv_bfloat162 *>(&y.y) = __floats2bfloat162_rn(acc.z * r, acc.w * r);
-            *reinterpret_cast<uint2 *>(a.out + it.b * a.ldo + static_cast<int64_t>(h) * D + dd) = y;
-            if (a.lse && dd == 0)
-                a.lse[row] = dead ? NAN : (mx + log2f(sum)) * kLn2;
-        } else {
-            const int64_t at = row * a.chunks + it.chunk;
-            *reinterpret_cast<float4 *>(a.part + at * D + dd) = acc;
-            if (dd == 0)
-                a.part_ml[at] = make_float2(mx, dead ? NAN : sum);
+        put<D>(a, it, head, dd, mx, sum, acc);
+    }
+}
+
+// NaN in this warp's share of the block's items from number `from` on.  The table of items is not used:
+// warps that have given up no longer keep one another's pace, on which refilling it depends.
+template <int D, int MG>
+__device__ __noinline__ void give_up(const Shared<D, MG> &sm, const AttnArgs &a, int from, int tid)
+{
+    const int lane = tid & 31;
+    for (int first = from;; first += 32) {
+        const Item mine = make_item(a, sm, first + lane);
+        for (int l = 0; l < 32; ++l) {
+            Item it = {};
+            it.b = __shfl_sync(kFull, mine.b, l);
+            it.kvh = __shfl_sync(kFull, mine.kvh, l);
+            it.chunk = __shfl_sync(kFull, mine.chunk, l);
+            it.chunks = __shfl_sync(kFull, mine.chunks, l);
+            if (it.b < 0)
+                return;
+            for (int x = tid; x < a.group * (D / 4); x += 32 * kHelpers)
+                put<D>(a, it, x / (D / 4), x % (D / 4) * 4, NAN, NAN, make_float4(NAN, NAN, NAN, NAN));
         }
     }
 }
@@ -836,7 +877,10 @@ __device__ __forceinline__ void help(Shared<D, MG> &sm, const AttnArgs &a, int w
         const Item then = sm.items[(i + 2) % kItemRing];
         q.load(a, then, w);
         q.convert(a);
-        wait_for(sm, &sm.states[i & 1], (i >> 1) & 1);
+        if (!wait_for(sm, a, &sm.states[i & 1], (i >> 1) & 1)) {
+            give_up(sm, a, i, threadIdx.x - 32 * kConsumers);
+            break;
+        }
         if (then.b >= 0)
             q.store(sm, a, i & 1, w);   // every consumer has read item i's
         add_states(sm, a, now, Shared<D, MG>::kStates == 1 ? 0 : i & 1, threadIdx.x - 32 * kConsumers);
@@ -1091,9 +1135,24 @@ bi_status_t run_attention(const AttnArgs &a, const CUtensorMap &k_map, const CUt
                                                                                   : run_merge<D, 16>(a, stream);
 }
 
+std::atomic<uint64_t> wait_ns{kWaitNs};
+std::atomic<uint32_t> debug_skip_load{0};
+
 } // namespace
 
 extern "C" {
+
+bi_status_t bi_paged_decode_attention_set_wait_timeout(uint64_t timeout_ns)
+{
+    wait_ns = timeout_ns ? timeout_ns : kWaitNs;
+    return BI_OK;
+}
+
+bi_status_t bi_paged_decode_attention_debug_skip_load(uint32_t n)
+{
+    debug_skip_load = n;
+    return BI_OK;
+}
 
 size_t bi_paged_decode_attention_workspace_bytes(int64_t B, int Hq, int D, int64_t max_len)
 {
@@ -1161,6 +1220,10 @@ bi_status_t bi_paged_decode_attention(const bi_kv_cache_t *cache, const void *Q,
     a.page_shift = bi_kv::log2_of(cache->page_size);
     a.chunks = static_cast<int>(most_chunks(max_len));
     a.scale_m = std::frexp(scale, &a.scale_e) * kLog2e;
+    a.skip_load = debug_skip_load;
+    // two cycles a nanosecond, at or above the highest SM clock; a limit of centuries stays one
+    const uint64_t ns = wait_ns;
+    a.wait_cycles = ns > UINT64_MAX / 4 ? UINT64_MAX / 2 : 2 * ns;
     a.part = static_cast<float *>(workspace);
     a.part_ml = reinterpret_cast<float2 *>(a.part + B * Hq * a.chunks * cache->head_dim);
     CUtensorMap k_map, v_map;

@@ -456,9 +456,12 @@ __device__ __forceinline__ void write_huge(uint8_t *to, const uint4 *from, float
     }
 }
 
+// Blocks of an SM: tokens of a warp are held in registers.
+__host__ __device__ constexpr int append_blocks(int piece) { return piece == 16 ? 3 : 2; }
+
 // G warps a group, kPiece tokens a warp: G * kPiece = page_size.
 template <int D, int G, int kPiece>
-__global__ void __launch_bounds__(32 * kAppendWarps, kPiece == 16 ? 3 : 2) kv_append_kernel(const __grid_constant__ AppendArgs a)
+__global__ void __launch_bounds__(32 * kAppendWarps, append_blocks(kPiece)) kv_append_kernel(const __grid_constant__ AppendArgs a)
 {
     constexpr int kVecs = D / 8;             // 16-byte vectors of a row's head
     constexpr int kTokens = 32 / kVecs;      // tokens one load instruction covers
@@ -788,12 +791,13 @@ bi_status_t bi_kv_append_e4m3(const bi_kv_cache_t *cache, const void *K, int64_t
     a.heads = cache->num_heads;
     a.page_shift = bi_kv::log2_of(cache->page_size);
     // Rows per block: one, so that the runs of a decode step are written side by side, while all warps
-    // are resident at once (64 tokens, 8 heads, pages of 64: two rows 3.1 us, one 4.9 us); at most a
-    // warp's 32.
+    // are resident at once (64 tokens, 8 heads, pages of 64: two rows 3.1 us, one 4.9 us; 160 tokens,
+    // pages of 256: sixteen rows 5.6 us, eight 7.7 us); at most a warp's 32.
     const int64_t groups = 2 * static_cast<int64_t>(cache->num_heads);
     const int warps = cache->page_size == 256 ? 8 : cache->page_size / 16;
+    const int resident = kAppendWarps * append_blocks(cache->page_size == 256 ? 32 : 16);
     a.rows = 1;
-    while (a.rows < 32 && (T + a.rows - 1) / a.rows * groups * warps > 24 * static_cast<int64_t>(sms))
+    while (a.rows < 32 && (T + a.rows - 1) / a.rows * groups * warps > resident * static_cast<int64_t>(sms))
         a.rows *= 2;
     const int64_t blocks = (T + a.rows - 1) / a.rows;
     if (blocks > INT32_MAX / groups)

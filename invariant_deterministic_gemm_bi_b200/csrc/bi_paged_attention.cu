@@ -1131,8 +1131,8 @@ bi_status_t run_attention(const AttnArgs &a, const CUtensorMap &k_map, const CUt
     const int eights = (a.chunks + kEight - 1) / kEight;
     return eights <= 1   ? run_merge<D, 1>(a, stream)
            : eights <= 2 ? run_merge<D, 2>(a, stream)
-           : eights <= 4 || static_cast<int64_t>(a.b) * a.hq > INT64_C(4) * sms ? run_merge<D, 4>(a, stream)
-                                                                                  : run_merge<D, 16>(a, stream);
+           : eights <= 4 || static_cast<int64_t>(a.b) * a.hq > sms ? run_merge<D, 4>(a, stream)
+                                                                   : run_merge<D, 16>(a, stream);
 }
 
 std::atomic<uint64_t> wait_ns{kWaitNs};

@@ -74,7 +74,11 @@ constexpr int kEntries = 256;               // entries of the scanned chunk coun
 constexpr int kClasses = 4;                 // of chunks, by steps: 4 and more, 3, 2, 1
 constexpr int kItemBlock = 32;              // items whose table entries one warp makes at once
 constexpr int kItemRing = 4 * kItemBlock;   // entries of the items' table
-constexpr int kMaxBatch = 16384;            // sequences; an entry stands for several when there are more than entries
+// Sequences.  With more of them than entries an entry stands for several, up to 64, whose lengths are read
+// one after the other to find a chunk's.  The reads hide behind the items: 256 sequences of 200 tokens,
+// 8 heads of 128, take 33.2 us and 257 33.7; 2048 of 40 tokens, 2 heads of 64, 39 us, and 16384 339 us,
+// 1.4 and 1.5 us for each item of a block.
+constexpr int kMaxBatch = 16384;
 constexpr int64_t kMaxLen = INT64_C(1) << 30;   // positions of a sequence
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -1126,8 +1130,10 @@ bi_status_t run_attention(const AttnArgs &a, const CUtensorMap &k_map, const CUt
     if (st != BI_OK || a.chunks == 1)
         return st;
     // Warps for a head: one or two where no sequence can have more eights of chunks; else four, or sixteen
-    // (all eights at once) while there are so few heads that all warps are resident (2 x 100001,
-    // 64 heads: the call takes 73.4 us, with four 76.0; 3200 ragged heads: 58.6 us, with four 50.9).
+    // (all eights at once) while there is at most one head for an SM.  The call with four and with
+    // sixteen, 16/1 heads: 131000 positions, 32 heads in all 28.7 and 25.1 us, 128 heads 66.1 and 62.4,
+    // 256 heads 117.4 and 116.3; 40000 positions, 128 heads 32.5 and 31.4, 256 heads 48.0 and 48.8, 512
+    // heads 77.4 and 82.0; 20 ragged sequences of up to 30000, 640 heads 44.4 and 48.3.
     const int eights = (a.chunks + kEight - 1) / kEight;
     return eights <= 1   ? run_merge<D, 1>(a, stream)
            : eights <= 2 ? run_merge<D, 2>(a, stream)
@@ -1229,6 +1235,8 @@ bi_status_t bi_paged_decode_attention(const bi_kv_cache_t *cache, const void *Q,
     CUtensorMap k_map, v_map;
     if ((st = bi_kv::page_map(&k_map, cache, cache->k)) != BI_OK || (st = bi_kv::page_map(&v_map, cache, cache->v)) != BI_OK)
         return st;
+    // Groups of up to four heads of 128 have a kernel of their own: 16 x 4096 of 4 heads takes 30.8 us, in
+    // the kernel for eight 31.2, of 2 heads 31.3 and 31.5 (less work for the helper warps; elsewhere equal).
     if (cache->head_dim == 128)
         return a.group <= 4   ? run_attention<128, 4>(a, k_map, v_map, dev, sms, stream)
                : a.group <= 8 ? run_attention<128, 8>(a, k_map, v_map, dev, sms, stream)

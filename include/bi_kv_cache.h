@@ -64,8 +64,9 @@ typedef struct {
  *      positions[t] = ctx + j and slot_map[t] = its slot.  The rows of slot_map and positions from
  *      token_offsets[B] to max_tokens are set to -1;
  *   4. *free_left = the pages left on the stack.
- * Entries of block_table that get no page, and of free_pages above the old and new top, keep
- * what they held.  All of it is integer work in a fixed order.
+ * Entries of block_table that get no page keep what they held, as do those of free_pages that step 1
+ * does not push to (a page that step 2 pops stays in its entry).  All of it is integer work in a fixed
+ * order.
  *
  * *status (device) is set to BI_OK; to BI_ERR_INVALID_ARG for a length below 0 (new_lens: below
  * -1) or a *free_count outside [0, free_capacity]; or to BI_ERR_UNSUPPORTED_SHAPE when the call

@@ -93,6 +93,14 @@ def test_the_page_is_a_function_of_its_tokens():
     assert np.isnan(c.value[[0, 2]]).all() and np.all(c.scale[[0, 2]] == 8.0)
 
 
+def test_popped_pages_stay_in_the_stacks_entries():
+    # one page comes back and three go: the old top is 2, the new one 0, and the pushed page's entry keeps it
+    table = np.array([[9, -1], [-1, -1], [-1, -1], [-1, -1]])
+    got = okv.block_tables([3, 0, 0, 0], [-1, 1, 1, 1], 16, [4, 5, -7, -8], 2, table, 3)
+    assert got["stack"].tolist() == [4, 5, 9, -8] and got["left"] == 0
+    assert got["table"][1:, 0].tolist() == [9, 5, 4] and got["table"][0, 0] == 9
+
+
 def test_attention_reads_the_paged_positions():
     g = np.random.default_rng(4)
     pages, page, heads, D, n = 9, 16, 2, 64, 50

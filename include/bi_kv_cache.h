@@ -11,8 +11,9 @@
  *   value(page p, token i, head h, d) = e4m3(code) * scale[p][h].
  *
  * Batch invariance reaches into the cache: a page's codes and scales are a function of the tokens
- * written to it alone.  They do not depend on the other sequences, on the page's number, or on
- * whether the tokens came one at a time, in pieces or all at once (see bi_kv_append_e4m3).
+ * written to it since its first place was, alone.  They do not depend on the other sequences, on the
+ * page's number, or on whether the tokens came one at a time, in pieces or all at once (see
+ * bi_kv_append_e4m3, also for tokens that are discarded and written over).
  *
  * Pointers are device pointers of the current device, owned by the caller; calls are asynchronous
  * on `stream` and allocate nothing.  Status codes are those of bi_gemm.h; a refused call has
@@ -108,6 +109,11 @@ bi_status_t bi_kv_block_tables(const int32_t *ctx_lens, const int32_t *new_lens,
  * the code the token would have got at once, and the page is a function of its tokens alone.  The
  * cut costs at most 2^-9 of the scale, 2^-16 of the head's largest magnitude.
  * Infinities and NaN are stored as NaN.
+ * Writing a place again.  E only grows until the page is started anew, so the page then keeps the
+ * exponent, and the rounding of the codes before that place, that the discarded token gave it: the codes
+ * are those of R(x / 2^E) for that E, no finer.  A sequence whose length goes back (draft tokens that were
+ * rejected) is the function of its final tokens that a sequence without them is only if the page of its
+ * new end is written again from that page's first place; a page that is new since then always is.
  *
  * Contract: the slots of one page in one call are consecutive rows with consecutive slots, as
  * bi_kv_block_tables gives them (one run per page), and the places before a run's first slot hold

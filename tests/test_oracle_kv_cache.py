@@ -93,6 +93,21 @@ def test_the_page_is_a_function_of_its_tokens():
     assert np.isnan(c.value[[0, 2]]).all() and np.all(c.scale[[0, 2]] == 8.0)
 
 
+def test_a_place_written_again_joins_what_was_there():
+    g = np.random.default_rng(5)
+    x = torch.from_numpy(g.standard_normal((12, 1, 64)).astype(np.float32)).to(torch.bfloat16)
+    x[8:] *= 64
+    bits, xd = inputs.to_numpy_bits(x), x.double().numpy()
+    c = okv.Cache(np.full((1, 16, 1, 64), 0x7F), np.full((1, 1), 8.0))
+    c.append(bits, np.arange(12))
+    c.append(bits[:2], np.array([8, 9]))             # two small tokens over the first large ones
+    e = okv.exponent(xd.ravel())                     # that of all tokens the page has seen
+    assert c.scale[0, 0] == 2.0 ** e and e > okv.exponent(xd[:8].ravel())
+    assert np.array_equal(c.value[0, :10, 0], okv.round_code(np.concatenate([xd[:8], xd[:2]])[:, 0] / 2.0 ** e))
+    c.append(bits[:8], np.arange(8))                 # from the first place: the page starts anew
+    assert c.scale[0, 0] == 2.0 ** okv.exponent(xd[:8].ravel())
+
+
 def test_popped_pages_stay_in_the_stacks_entries():
     # one page comes back and three go: the old top is 2, the new one 0, and the pushed page's entry keeps it
     table = np.array([[9, -1], [-1, -1], [-1, -1], [-1, -1]])

@@ -190,11 +190,17 @@ def _check(status: int, where: str):
         raise BiGemmError(status, where)
 
 
+def _current_stream(torch, device: int) -> int:
+    """The handle of torch.cuda.current_stream(device): where torch has its private way to it, which
+    makes no Stream object (3 us), by that, else by the public one."""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
+
+
 def _stream_handle(stream) -> int | None:
     if stream is None:
         import torch
-        # the handle of torch.cuda.current_stream(), without making a Stream object (3 us)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _current_stream(torch, torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -531,7 +537,7 @@ def _current_device(torch) -> int:
 
 def _stream_on(torch, device, stream):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device) if device >= 0 else None
+        return _current_stream(torch, device) if device >= 0 else None
     return _stream_handle(stream)
 
 

@@ -653,6 +653,8 @@ def bi_paged_decode_attention(cache: KvCache, Q, block_table, seq_lens, O, scale
     bi_paged_decode_attention_workspace_bytes(B, Hq, D, max_pages * page_size) bytes."""
     import torch
     device = _current_device(torch)
+    if Q.dim() != 3:
+        raise TypeError("Q must be [B, Hq, D]")
     Hq = Q.shape[1]
     B, ldq = _heads_rows(torch, "Q", Q, device, Hq, cache.head_dim)
     rows, ldo = _heads_rows(torch, "O", O, device, Hq, cache.head_dim)

@@ -146,3 +146,12 @@ def test_the_binding_refuses_what_the_abi_cannot_see():
                    {"free_count": n}, {"free_left": n}, {"status": n}, {"positions": one}, {"slot_map": i4.float()}):
         with pytest.raises((TypeError, ValueError)):
             bg.bi_kv_block_tables(**(good | change))
+
+
+@pytest.mark.parametrize("shape", [(64,), (2, 256), (1, 2, 4, 64), ()])
+def test_queries_of_other_shapes_are_refused(shape):
+    k, s = torch.zeros((3, 16, 2, 64), dtype=torch.uint8), torch.ones((3, 2))
+    c = bg.KvCache(k, k.clone(), s, s.clone())
+    Q = torch.zeros(shape, dtype=torch.bfloat16)
+    with pytest.raises(TypeError):
+        bg.bi_paged_decode_attention(c, Q, torch.zeros((2, 3), dtype=torch.int32), torch.zeros(2, dtype=torch.int32), Q, 0.1)

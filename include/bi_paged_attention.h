@@ -17,6 +17,12 @@
  * A sequence with L = 0 gets O = 0 and lse = -inf.  L outside [0, max_pages * page_size], a page
  * number outside [0, num_pages) or a scale outside [2^-64, 2^64] among the attended positions make
  * the sequence's outputs (a scale: its key/value head's) NaN, and nothing is read out of bounds.
+ *
+ * Accuracy: sums, softmax statistics and scores are fp32.  In the sum over v_j the weights are fp16, off
+ * by up to 2^-11 of themselves with signs that vary (weight times value scale below 2^-29 of the
+ * sequence's largest: by 2^-40 of that), before O is rounded to bf16, up to 2^-8.  lse and the
+ * denominator do not see it.  bi_decode_attention keeps fp32 weights.
+ *
  * Codes behind position L - 1, NaN among them, and pages wholly before the window are never read
  * into a result.  Several query tokens of one sequence are sequences of their own that share a
  * table row's contents, each with its own length.

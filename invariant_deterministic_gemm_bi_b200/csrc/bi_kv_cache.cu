@@ -745,8 +745,9 @@ bi_status_t bi_kv_block_tables(const int32_t *ctx_lens, const int32_t *new_lens,
     if (st != BI_OK)
         return st;
     const size_t smem = table_smem_bytes(B);
-    // CTAs: one for every 4096 tokens, up to the largest cluster.  51k tokens of 1000 requests take
-    // 10.3 us with 8 CTAs and 8.0 with 16; 69k of 33 prompts 8.1 and 6.3.  (Eight tokens a thread: 9.3.)
+    // CTAs: one for every 4096 tokens, up to the largest cluster.  51k tokens of 1000 requests took
+    // 10.3 us with 8 CTAs and 8.0 with 16, 69k of 33 prompts 8.1 and 6.3 (8.4 and 6.6 since threads search
+    // again).  Eight tokens a thread: 9.3.
     int cluster = 1;
     while (cluster < largest && static_cast<int64_t>(cluster) * kTableThreads * kTableTokens < (max_tokens > B ? max_tokens : B))
         cluster *= 2;

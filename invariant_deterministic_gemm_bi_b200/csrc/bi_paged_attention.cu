@@ -27,14 +27,13 @@
 // inside a 16-byte group is permuted alike on both sides, so codes go from ldmatrix to the
 // conversion without shuffles; values are read transposed, two dimensions to a 16-bit element.
 // tcgen05 would need the weights and queries split into several e4m3 parts, or the codes written
-// back to shared memory as fp16.  Without loads the kernel takes 74 us for 64 sequences of 4096
-// positions, without products and softmax 86 us, whole 92 us and the merge 3: the loads bound it
-// (5.9 TB/s).  Where sequences are short or ragged the products do: conversions and byte permutations
+// back to shared memory as fp16.  For 64 sequences of 4096 positions the call takes 97 us (5.5 TB/s), 3 of
+// them the merge; without loads 79, without products and softmax 89: the loads bound it.  Where sequences are short or ragged the products do: conversions and byte permutations
 // issue every second cycle, an m16n8k16 every eighth, and they do not overlap.
 //
 // Weights.  With sv the value scale of a position's page, the state's maximum M is that of
 // t_j = s_j log2 e + log2 sv, and the weight of a value's code is a_j = 2^(t_j - M + 15) <= 2^15,
-// rounded to fp16 (2^-11 of itself, a quarter of what bf16 would cost; the output is rounded to bf16
+// rounded to fp16 (2^-11 of itself, an eighth of what bf16 would cost; the output is rounded to bf16
 // anyway).  The value scale so costs nothing per element and weights down to 2^-29 of the largest keep
 // all of fp16's bits.  The softmax sum adds 2^(s_j log2 e - M) in fp32.  With scales from 2^-64 to 2^64
 // a position may count in it although t_j is far below M: by 128 for the scales and 54 for the score

@@ -18,7 +18,8 @@
  * number outside [0, num_pages) or a scale outside [2^-64, 2^64] among the attended positions make
  * the sequence's outputs (a scale: its key/value head's) NaN, and nothing is read out of bounds.
  *
- * Accuracy: sums, softmax statistics and scores are fp32.  In the sum over v_j the weights are fp16, off
+ * Accuracy: sums, softmax statistics and scores are fp32.  Entries of a query head below 2^-28 of its
+ * largest are off by up to 2^-39 of that largest, all others exact.  In the sum over v_j the weights are fp16, off
  * by up to 2^-11 of themselves with signs that vary (weight times value scale below 2^-29 of the
  * sequence's largest: by 2^-40 of that), before O is rounded to bf16, up to 2^-8.  lse and the
  * denominator do not see it.  bi_decode_attention keeps fp32 weights.

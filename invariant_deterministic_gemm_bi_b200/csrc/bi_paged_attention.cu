@@ -22,8 +22,9 @@
 // Matrix products.  The cache is the first operand of mma.m16n8k16 (16 positions, or 16 dimensions,
 // a time) and the query heads are the 8 columns, so grouped queries fill the tile instead of
 // padding it to 16 rows.  e4m3 codes become fp16 exactly; queries become fp16 exactly after a power
-// of two per head has been taken out of them (bf16 has fewer significant bits; entries below 2^-29
-// of the head's largest lose bits that are below the fp32 sum's own).  The order of dimensions
+// of two per head has been taken out of them (bf16 has fewer significant bits; entries below 2^-28 of the
+// head's largest are off by up to 2^-39 of it, which an fp32 sum loses anyway unless the keys are zero
+// where the query is large).  The order of dimensions
 // inside a 16-byte group is permuted alike on both sides, so codes go from ldmatrix to the
 // conversion without shuffles; values are read transposed, two dimensions to a 16-bit element.
 // tcgen05 would need the weights and queries split into several e4m3 parts, or the codes written

@@ -144,3 +144,24 @@ def test_scores_inside_fp32_of_factors_beyond_it(scale, q, k_scale):
         assert torch.equal(O[0], v.expand(2, -1)), best
         assert torch.all((lse.double() - s).abs() <= 2.0 ** -21 * abs(s))
         rows[:n, 0, 0] = codes
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("down,scale", [(28, 2.0 ** 28), (20, 2.0 ** 20), (34, 2.0 ** 30)])
+def test_small_entries_beside_a_large_one_that_meets_zero_keys(dim, down, scale):
+    """Entries down to 2^-28 of the head's largest are exact; below, a score is off by up to scale * 2^-39 of the
+    largest times sum |k|, which moves a weight by as much."""
+    cache, table, lens = sequence(400, 1, dim, 32, seed=25)
+    cache.k.copy_(gaussian_codes(cache.k.shape, 26))
+    cache.k[..., 0] = 0
+    Q = (queries(1, 4, dim, 27).float().clamp(-1.9, 1.9) * 2.0 ** -down).to(torch.bfloat16)
+    if down == 28:   # magnitudes in [1, 2), so that every entry is at or above 2^-28
+        Q = (Q.float() + torch.sign(Q.float()) * 2.0 ** -down).clamp(-1.99 * 2.0 ** -down, 1.99 * 2.0 ** -down).to(torch.bfloat16)
+    Q[..., 0] = 1
+    O, lse = attend(cache, Q, table, lens, scale)
+    ref = list(oracle(cache, Q, table, lens, scale))
+    if down > 28:
+        k = okv.Cache(cache.k.cpu().numpy(), cache.k_scale.cpu().numpy()).dequantised()
+        # ds = 2^-23 (D + 4) |scale| mass in the bound: mass grows by what the entries may be off
+        ref[3] = ref[3] + np.abs(k).sum(-1).max() * 2.0 ** -39 * 2.0 ** 23 / (dim + 4)
+    assert_attention(O, lse, ref, scale, dim)
